@@ -6,4 +6,5 @@ package does not load the library; the first call does, and fails loudly if
 it has not been built.
 """
 from . import llsa  # noqa: F401
-from .llsa import BF16, FP32, LLSAError, Pipeline, Problem  # noqa: F401
+from .llsa import (BF16, FP32, CrossAttention, CrossProblem, LayerNorm, LLSAError, NormProblem,  # noqa: F401
+                   Pipeline, Problem)

@@ -16,6 +16,18 @@ CUDA tensors (or raw device addresses as ints):
 
 ``Pipeline`` allocates the buffers of one problem once and runs the whole
 path (pool -> select -> attend -> transpose -> backward) through these calls.
+
+Beside the self-attention, for conditional models, with the same manner of use:
+
+    cross_attn_fwd(problem, q, k, v, o, lse, kv_len, key_mask, workspace)
+    cross_attn_bwd(problem, q, k, v, o, dO, lse, dq, dk, dv, kv_len, key_mask, workspace)
+    layer_norm_fwd(problem, x, weight, bias, y, mean, rstd)
+    layer_norm_bwd(problem, x, dy, weight, mean, rstd, dx, dweight, dbias, workspace)
+
+``CrossAttention`` and ``LayerNorm`` allocate one problem's buffers and run the
+forward and the backward.  These calls take tensors with any batch, head and
+token strides, check every tensor's shape, type and device, and run on the
+tensors' device, on its current torch stream unless one is given.
 """
 from __future__ import annotations
 
@@ -36,7 +48,9 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "shape", 3: "alignment", 4: "worksp
 EXPORTS = ("llsa_status_string", "llsa_validate", "llsa_level_sizes", "llsa_query_sizes", "llsa_reorder",
            "llsa_pool", "llsa_select", "llsa_select_level", "llsa_attn_fwd", "llsa_index_transpose",
            "llsa_attn_bwd", "llsa_device_error", "llsa_kernel_launches", "llsa_index_transpose_noalloc",
-           "llsa_selftest_wait_timeout", "llsa_attn_paths")
+           "llsa_selftest_wait_timeout", "llsa_attn_paths", "llsa_cross_validate", "llsa_cross_query_sizes",
+           "llsa_cross_attn_fwd", "llsa_cross_attn_bwd", "llsa_cross_attn_paths", "llsa_norm_validate",
+           "llsa_norm_query_sizes", "llsa_layer_norm_fwd", "llsa_layer_norm_bwd")
 
 
 class LLSAError(RuntimeError):
@@ -58,6 +72,31 @@ class CSizes(ctypes.Structure):
                                                 "bwd_workspace_bytes")]
 
 
+class CStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class CCrossProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int)] + \
+               [(n, CStrides) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")]
+
+
+class CCrossBuffers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("lse_bytes", "fwd_workspace_bytes", "bwd_workspace_bytes")]
+
+
+class CNormProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "n", "c")] + [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int) for n in ("dtype", "param_dtype", "per_batch")] + \
+               [(n, CStrides) for n in ("x", "y", "dy", "dx")] + \
+               [(n, ctypes.c_int64) for n in ("weight_batch", "bias_batch")]
+
+
+class CNormBuffers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("stat_bytes", "bwd_workspace_bytes")]
+
+
 _lib = None
 
 
@@ -70,6 +109,7 @@ def lib() -> ctypes.CDLL:
                                "(nvcc, sm_100a); there is no fallback path")
         L = ctypes.CDLL(LIB_PATH)
         P = ctypes.POINTER(CProblem)
+        X, M = ctypes.POINTER(CCrossProblem), ctypes.POINTER(CNormProblem)
         vp, i32 = ctypes.c_void_p, ctypes.c_int
         sig = {
             "llsa_status_string": ([i32], ctypes.c_char_p),
@@ -88,6 +128,15 @@ def lib() -> ctypes.CDLL:
             "llsa_kernel_launches": ([], ctypes.c_uint64),
             "llsa_selftest_wait_timeout": ([ctypes.c_uint, i32, i32, vp], i32),
             "llsa_attn_paths": ([P, ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
+            "llsa_cross_validate": ([X], i32),
+            "llsa_cross_query_sizes": ([X, ctypes.POINTER(CCrossBuffers)], i32),
+            "llsa_cross_attn_fwd": ([X] + [vp] * 9, i32),
+            "llsa_cross_attn_bwd": ([X] + [vp] * 13, i32),
+            "llsa_cross_attn_paths": ([X, ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
+            "llsa_norm_validate": ([M], i32),
+            "llsa_norm_query_sizes": ([M, ctypes.POINTER(CNormBuffers)], i32),
+            "llsa_layer_norm_fwd": ([M] + [vp] * 7, i32),
+            "llsa_layer_norm_bwd": ([M] + [vp] * 10, i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -321,3 +370,327 @@ class Pipeline:
         self.forward(q, k, v, stream)
         if dO is not None:
             self.backward_pass(q, k, v, dO, stream)
+
+
+# ------------------------------------------------------------------ cross attention and layer norm
+
+def _checked(name: str, x, shape, dtype: int, device):
+    """x as this call takes it: a CUDA tensor of this shape and type whose last dimension is contiguous."""
+    if tuple(x.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
+    if x.dtype != _torch_dtype(dtype):
+        raise ValueError(f"{name}: {x.dtype}, expected {_torch_dtype(dtype)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, expected {device}")
+    if shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension is not contiguous")
+    return x.data_ptr()
+
+
+def _flat(name: str, x, shape, dtype, device):
+    """A contiguous tensor of this shape (or an int address, or None)."""
+    if x is None or isinstance(x, int):
+        return x
+    if tuple(x.shape) != shape or x.dtype != dtype or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
+                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _work(x, nbytes: int, device):
+    if x is None or isinstance(x, int):
+        return x
+    if x.device != device or x.numel() * x.element_size() < nbytes or not x.is_contiguous():
+        raise ValueError(f"workspace: expected {nbytes} contiguous bytes on {device}")
+    return x.data_ptr()
+
+
+def _torch_dtype(dtype: int):
+    import torch
+    return torch.bfloat16 if dtype == BF16 else torch.float32
+
+
+def _strided(name: str, cs: CStrides, x):
+    s = x.stride()
+    if s[0] == s[1] == s[2] == 0 and x.shape[:3].numel() > 1:      # zeros stand for the contiguous layout
+        raise ValueError(f"{name}: one token expanded over every dimension; materialise at least one of them")
+    cs.batch, cs.head, cs.token = s[0], s[1], s[2]
+
+
+class _On:
+    """The tensors' device as the current one, and the stream of a call: the given one, else the device's current one."""
+
+    __slots__ = ("index", "before", "stream")
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors on {device}: these calls take CUDA tensors")
+        self.index = device.index
+        self.before = torch.cuda.current_device()
+        if stream is None:
+            stream = torch.cuda.current_stream(self.index)
+        self.stream = stream if isinstance(stream, int) else stream.cuda_stream
+
+    def __enter__(self):
+        if self.before != self.index:
+            import torch
+            torch.cuda.set_device(self.index)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            import torch
+            torch.cuda.set_device(self.before)
+
+
+@dataclass
+class CrossProblem:
+    """Fields of llsa_cross_problem; kv_heads defaults to heads, scale to 1/sqrt(d).  Strides come from the tensors."""
+    batch: int
+    heads: int
+    nq: int
+    nk: int
+    d: int = 64
+    kv_heads: Optional[int] = None
+    scale: Optional[float] = None
+    dtype: int = BF16
+
+    def __post_init__(self):
+        if self.kv_heads is None:
+            self.kv_heads = self.heads
+        if self.scale is None:
+            self.scale = 1.0 / sqrt(self.d) if self.d > 0 else 0.0
+
+    @property
+    def q_shape(self):
+        return (self.batch, self.heads, self.nq, self.d)
+
+    @property
+    def k_shape(self):
+        return (self.batch, self.kv_heads, self.nk, self.d)
+
+    def c(self) -> CCrossProblem:
+        return CCrossProblem(self.batch, self.heads, self.kv_heads, self.nq, self.nk, self.d, float(self.scale),
+                             self.dtype)
+
+
+def cross_validate(p: CrossProblem) -> int:
+    return lib().llsa_cross_validate(ctypes.byref(p.c()))
+
+
+def cross_query_sizes(p: CrossProblem) -> dict:
+    s = CCrossBuffers()
+    _check(lib().llsa_cross_query_sizes(ctypes.byref(p.c()), ctypes.byref(s)), "cross_query_sizes")
+    return {name: getattr(s, name) for name, _ in CCrossBuffers._fields_}
+
+
+def cross_attn_paths(p: CrossProblem) -> dict:
+    """Which kernels cross_attn_fwd / cross_attn_bwd run for p: "tensor" or "cuda-core"."""
+    f, b = ctypes.c_int(0), ctypes.c_int(0)
+    _check(lib().llsa_cross_attn_paths(ctypes.byref(p.c()), ctypes.byref(f), ctypes.byref(b)), "cross_attn_paths")
+    name = {1: "tensor", 0: "cuda-core"}
+    return {"fwd": name[f.value], "bwd": name[b.value]}
+
+
+def _cross_args(p: CrossProblem, named, kv_len, key_mask):
+    """The C problem with the tensors' strides, their addresses, and the addresses of kv_len and key_mask."""
+    import torch
+    c = p.c()
+    device = named[0][1].device
+    qs, ks = p.q_shape, p.k_shape
+    ptrs = []
+    for name, x in named:
+        ptrs.append(_checked(name, x, ks if name in ("k", "v", "dk", "dv") else qs, p.dtype, device))
+        _strided(name, getattr(c, "d_o" if name == "dO" else name), x)
+    n = _flat("kv_len", kv_len, (p.batch,), torch.int32, device)
+    m = key_mask
+    if m is not None and not isinstance(m, int) and m.dtype == torch.bool:
+        m = m.view(torch.uint8)
+    return c, device, ptrs, n, _flat("key_mask", m, (p.batch, p.nk), torch.uint8, device)
+
+
+def cross_attn_fwd(p: CrossProblem, q, k, v, o, lse=None, kv_len=None, key_mask=None, workspace=None, stream=None):
+    """q, o: [batch, heads, nq, d]; k, v: [batch, kv_heads, nk, d]; lse: fp32 [batch, heads, nq] or None; kv_len:
+    int32 [batch] or None; key_mask: bool or uint8 [batch, nk], nonzero where the key is attended to, or None;
+    workspace: fwd_workspace_bytes of device memory."""
+    import torch
+    c, device, a, n, m = _cross_args(p, (("q", q), ("k", k), ("v", v), ("o", o)), kv_len, key_mask)
+    ls = _flat("lse", lse, p.q_shape[:3], torch.float32, device)
+    need = cross_query_sizes(p)["fwd_workspace_bytes"]
+    with _On(device, stream) as s:
+        _check(lib().llsa_cross_attn_fwd(ctypes.byref(c), a[0], a[1], a[2], n, m, a[3], ls,
+                                         _work(workspace, need, device), s), "cross_attn_fwd")
+
+
+def cross_attn_bwd(p: CrossProblem, q, k, v, o, dO, lse, dq, dk, dv, kv_len=None, key_mask=None, workspace=None,
+                   stream=None):
+    """Gradients of cross_attn_fwd for the same kv_len and key_mask; workspace: bwd_workspace_bytes."""
+    import torch
+    c, device, a, n, m = _cross_args(p, (("q", q), ("k", k), ("v", v), ("o", o), ("dO", dO), ("dq", dq), ("dk", dk),
+                                         ("dv", dv)), kv_len, key_mask)
+    ls = _flat("lse", lse, p.q_shape[:3], torch.float32, device)
+    need = cross_query_sizes(p)["bwd_workspace_bytes"]
+    with _On(device, stream) as s:
+        _check(lib().llsa_cross_attn_bwd(ctypes.byref(c), a[0], a[1], a[2], n, m, a[3], a[4], ls, a[5], a[6], a[7],
+                                         _work(workspace, need, device), s), "cross_attn_bwd")
+
+
+def _buffer(shape, dtype, device, token_major: bool):
+    """A [batch, heads, tokens, d] tensor, in memory as such or (token_major) as [batch, tokens, heads, d]."""
+    import torch
+    if not token_major:
+        return torch.empty(shape, dtype=dtype, device=device)
+    b, h, n, d = shape
+    return torch.empty((b, n, h, d), dtype=dtype, device=device).transpose(1, 2)
+
+
+class CrossAttention:
+    """Buffers of one cross-attention problem, allocated once, and its passes.  With token_major, o and the gradients
+    lie in memory as [batch, tokens, heads, d], as the projections around the attention have them."""
+
+    def __init__(self, p: CrossProblem, device="cuda", backward: bool = True, token_major: bool = False):
+        import torch
+        self.p = p
+        _check(cross_validate(p), "cross_validate")
+        self.sizes = cross_query_sizes(p)
+        dt = _torch_dtype(p.dtype)
+        self.o = _buffer(p.q_shape, dt, device, token_major)
+        self.lse = torch.empty(p.q_shape[:3], dtype=torch.float32, device=device)
+        need = max(self.sizes["fwd_workspace_bytes"], self.sizes["bwd_workspace_bytes"] if backward else 0)
+        self.work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        self.backward = backward
+        if backward:
+            self.dq = _buffer(p.q_shape, dt, device, token_major)
+            self.dk = _buffer(p.k_shape, dt, device, token_major)
+            self.dv = _buffer(p.k_shape, dt, device, token_major)
+
+    def forward(self, q, k, v, kv_len=None, key_mask=None, stream=None):
+        cross_attn_fwd(self.p, q, k, v, self.o, self.lse, kv_len, key_mask, self.work, stream)
+        return self.o, self.lse
+
+    def backward_pass(self, q, k, v, dO, kv_len=None, key_mask=None, stream=None):
+        """The gradients of the last forward call's problem (its o and lse are read)."""
+        cross_attn_bwd(self.p, q, k, v, self.o, dO, self.lse, self.dq, self.dk, self.dv, kv_len, key_mask, self.work,
+                       stream)
+        return self.dq, self.dk, self.dv
+
+
+@dataclass
+class NormProblem:
+    """Fields of llsa_norm_problem; param_dtype defaults to dtype.  Strides come from the tensors."""
+    batch: int
+    heads: int
+    n: int
+    c: int
+    eps: float = 1e-6
+    dtype: int = BF16
+    param_dtype: Optional[int] = None
+    per_batch: bool = False
+
+    def __post_init__(self):
+        if self.param_dtype is None:
+            self.param_dtype = self.dtype
+
+    @property
+    def shape(self):
+        return (self.batch, self.heads, self.n, self.c)
+
+    @property
+    def param_shape(self):
+        return (self.batch, self.c) if self.per_batch else (self.c,)
+
+    def cp(self) -> CNormProblem:
+        return CNormProblem(self.batch, self.heads, self.n, self.c, float(self.eps), self.dtype, self.param_dtype,
+                            int(self.per_batch))
+
+
+def norm_validate(p: NormProblem) -> int:
+    return lib().llsa_norm_validate(ctypes.byref(p.cp()))
+
+
+def norm_query_sizes(p: NormProblem) -> dict:
+    s = CNormBuffers()
+    _check(lib().llsa_norm_query_sizes(ctypes.byref(p.cp()), ctypes.byref(s)), "norm_query_sizes")
+    return {name: getattr(s, name) for name, _ in CNormBuffers._fields_}
+
+
+def _norm_args(p: NormProblem, named):
+    c = p.cp()
+    device = named[0][1].device
+    ptrs = []
+    for name, x in named:
+        if x is None:
+            ptrs.append(None)
+            continue
+        ptrs.append(_checked(name, x, p.shape, p.dtype, device))
+        _strided(name, getattr(c, name), x)
+    return c, device, ptrs
+
+
+def _param(p: NormProblem, c: CNormProblem, name: str, x, device):
+    """weight or bias: [c] contiguous, or [batch, c] with its rows apart by any stride."""
+    if x is None or isinstance(x, int):
+        return x
+    address = _checked(name, x, p.param_shape, p.param_dtype, device)
+    if p.per_batch:
+        if p.batch > 1 and x.stride(0) == 0:                # zero stands for contiguous rows
+            raise ValueError(f"{name}: one row expanded over the batch; per_batch=False takes it as [c]")
+        setattr(c, name + "_batch", x.stride(0) if p.batch > 1 else 0)
+    return address
+
+
+def layer_norm_fwd(p: NormProblem, x, weight, bias, y, mean=None, rstd=None, stream=None):
+    """x, y: [batch, heads, n, c]; weight, bias: [c] (per_batch: [batch, c], rows any
+    stride apart) or None; mean, rstd: fp32 [batch, heads, n] or None."""
+    import torch
+    c, device, a = _norm_args(p, (("x", x), ("y", y)))
+    f = [_param(p, c, name, t, device) for name, t in (("weight", weight), ("bias", bias))]
+    st = [_flat(name, t, p.shape[:3], torch.float32, device) for name, t in (("mean", mean), ("rstd", rstd))]
+    with _On(device, stream) as s:
+        _check(lib().llsa_layer_norm_fwd(ctypes.byref(c), a[0], f[0], f[1], a[1], st[0], st[1], s), "layer_norm_fwd")
+
+
+def layer_norm_bwd(p: NormProblem, x, dy, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None,
+                   stream=None):
+    """Gradients of layer_norm_fwd; dx, dweight and dbias are written where given; workspace: bwd_workspace_bytes."""
+    import torch
+    c, device, a = _norm_args(p, (("x", x), ("dy", dy), ("dx", dx)))
+    pt = _torch_dtype(p.param_dtype)
+    f = [_param(p, c, "weight", weight, device)]
+    f += [_flat(name, t, p.param_shape, pt, device) for name, t in (("dweight", dweight), ("dbias", dbias))]
+    st = [_flat(name, t, p.shape[:3], torch.float32, device) for name, t in (("mean", mean), ("rstd", rstd))]
+    need = norm_query_sizes(p)["bwd_workspace_bytes"]
+    with _On(device, stream) as s:
+        _check(lib().llsa_layer_norm_bwd(ctypes.byref(c), a[0], a[1], f[0], st[0], st[1], a[2], f[1], f[2],
+                                         _work(workspace, need, device), s), "layer_norm_bwd")
+
+
+class LayerNorm:
+    """Buffers of one layer-norm problem, allocated once, and its passes (token_major as for CrossAttention)."""
+
+    def __init__(self, p: NormProblem, device="cuda", backward: bool = True, token_major: bool = False):
+        import torch
+        self.p = p
+        _check(norm_validate(p), "norm_validate")
+        dt, pt = _torch_dtype(p.dtype), _torch_dtype(p.param_dtype)
+        self.y = _buffer(p.shape, dt, device, token_major)
+        self.backward = backward
+        self.mean = self.rstd = None
+        if backward:
+            self.mean = torch.empty(p.shape[:3], dtype=torch.float32, device=device)
+            self.rstd = torch.empty(p.shape[:3], dtype=torch.float32, device=device)
+            self.dx = _buffer(p.shape, dt, device, token_major)
+            self.dweight = torch.empty(p.param_shape, dtype=pt, device=device)
+            self.dbias = torch.empty(p.param_shape, dtype=pt, device=device)
+            self.work = torch.empty(norm_query_sizes(p)["bwd_workspace_bytes"], dtype=torch.uint8, device=device)
+
+    def forward(self, x, weight=None, bias=None, stream=None):
+        layer_norm_fwd(self.p, x, weight, bias, self.y, self.mean, self.rstd, stream)
+        return self.y
+
+    def backward_pass(self, x, weight, dy, stream=None):
+        """The gradients of the last forward call (its mean and rstd are read)."""
+        layer_norm_bwd(self.p, x, dy, weight, self.mean, self.rstd, self.dx, self.dweight, self.dbias, self.work,
+                       stream)
+        return self.dx, self.dweight, self.dbias

@@ -224,6 +224,122 @@ llsa_status llsa_device_error(llsa_stream stream, int* code);
  * launch. */
 llsa_status llsa_selftest_wait_timeout(unsigned limit_us, int code, int arrive, llsa_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Around the self-attention of a conditional diffusion transformer: cross
+ * attention to an encoder's states, and layer norm.
+ *
+ * These calls take token tensors [batch][heads][tokens][d] with element
+ * strides per batch row, head and token (the channels of a token are
+ * contiguous), so that slices of a projection's output are used in place.  A
+ * llsa_strides of zeros means the contiguous layout above.  An input may
+ * repeat itself (a stride of 0); tensors that are written may not overlap
+ * themselves (LLSA_ERR_ARG), nor any other argument unless a call says so.
+ * The buffers of cross attention and all workspaces are 16-byte aligned; those
+ * of layer norm need their element's alignment only (with 16 bytes, and widths
+ * and strides that are multiples of 8 elements, it is faster).
+ * The conventions at the top of this file hold otherwise: asynchronous on
+ * `stream`, on the current device, which owns every buffer; nothing is
+ * allocated and nothing kept.  A workspace may be used by one call at a time
+ * (give each graph that replays concurrently its own); its contents are
+ * ignored on entry.  Calls give the same bits every time.
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+  int64_t batch, head, token;   /* in elements */
+} llsa_strides;
+
+/* Cross attention: `nq` queries per head and batch row attend to the `nk`
+ * states of an encoder. */
+typedef struct {
+  int batch, heads;       /* of the queries */
+  int kv_heads;           /* of keys and values; divides heads: query head h reads key head h / (heads / kv_heads) */
+  int nq, nk;
+  int d;                  /* head dimension (multiple of 8, at most 128) */
+  float scale;            /* softmax scale; 0 selects 1/sqrt(d) */
+  int dtype;              /* llsa_dtype of q, k, v, o and of their gradients */
+  /* strides: multiples of 8 elements (bf16) or 4 (fp32) */
+  llsa_strides q, k, v, o, d_o, dq, dk, dv;
+} llsa_cross_problem;
+
+typedef struct {
+  size_t lse_bytes;               /* fp32 [batch][heads][nq] */
+  size_t fwd_workspace_bytes;     /* may be 0: then the workspace may be NULL */
+  size_t bwd_workspace_bytes;
+} llsa_cross_buffers;
+
+/* Checks every field of *p; no launch. */
+llsa_status llsa_cross_validate(const llsa_cross_problem* p);
+
+/* Byte sizes of lse and of the workspaces; they depend on the sizes and types
+ * in *p, not on its strides. */
+llsa_status llsa_cross_query_sizes(const llsa_cross_problem* p, llsa_cross_buffers* out);
+
+/* o_i = sum_j softmax_j(scale q_i . k_j) v_j over the batch row's valid keys,
+ * lse_i = log sum_j exp(scale q_i . k_j).  Key j of batch row b is valid when
+ * j < kv_len[b] and key_mask[b][j] != 0.  kv_len: int32 [batch] in device
+ * memory, 4-byte aligned, clamped to 0..nk, or NULL (all nk); key_mask: uint8
+ * [batch][nk] in device memory, or NULL (none masked).  k and v at keys that
+ * are not valid are never used, whatever they hold.  Without a valid key
+ * o = 0 and lse = -inf.  lse may be NULL. */
+llsa_status llsa_cross_attn_fwd(const llsa_cross_problem* p, const void* q, const void* k, const void* v,
+                                const int32_t* kv_len, const uint8_t* key_mask, void* o, float* lse,
+                                void* workspace, llsa_stream stream);
+
+/* Gradients of llsa_cross_attn_fwd.  With P = exp(z - lse), D_i = d_o_i . o_i
+ * and dS = scale P (d_o v^T - D): dq = dS k, dk = dS^T q, dv = P^T d_o, the
+ * last two summed over the query heads of a key head; zero for keys that are
+ * not valid and queries without a valid key.  o, lse: from the forward call
+ * with the same keys, kv_len and key_mask. */
+llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, const void* k, const void* v,
+                                const int32_t* kv_len, const uint8_t* key_mask, const void* o, const void* d_o,
+                                const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                                llsa_stream stream);
+
+/* Which kernels the two calls run for *p (host only, no launch): 1 for the
+ * tensor-core kernels, 0 for the CUDA-core ones.  Either pointer may be NULL. */
+llsa_status llsa_cross_attn_paths(const llsa_cross_problem* p, int* fwd_tc, int* bwd_tc);
+
+/* Layer norm of every token row over its c channels. */
+typedef struct {
+  int batch, heads, n;    /* rows: batch * heads * n */
+  int c;                  /* channels, 1..LLSA_NORM_MAX_C */
+  float eps;              /* added to the variance; >= 0 */
+  int dtype;              /* llsa_dtype of x, y, dy, dx */
+  int param_dtype;        /* of weight, bias and their gradients: dtype or LLSA_FP32 */
+  int per_batch;          /* 0: weight, bias [c]; 1: [batch][c], a modulation of its own for each batch row (strided, as
+                           * slices of a projection's output are) */
+  llsa_strides x, y, dy, dx;   /* any strides */
+  int64_t weight_batch, bias_batch; /* per_batch: elements between the batch rows; 0: c.  Not used otherwise */
+} llsa_norm_problem;
+
+#define LLSA_NORM_MAX_C 16384
+
+typedef struct {
+  size_t stat_bytes;              /* fp32 [batch][heads][n], mean and rstd each */
+  size_t bwd_workspace_bytes;
+} llsa_norm_buffers;
+
+llsa_status llsa_norm_validate(const llsa_norm_problem* p);
+/* Byte sizes; they depend on the sizes and types in *p, not on its strides. */
+llsa_status llsa_norm_query_sizes(const llsa_norm_problem* p, llsa_norm_buffers* out);
+
+/* y = (x - mean) * rstd * weight + bias with mean and rstd = 1 / sqrt(var + eps)
+ * over the row's channels (var: mean of the squared deviations).  weight and
+ * bias may be NULL (1 and 0); mean and rstd are written where not NULL.  y may
+ * be x itself with the same strides. */
+llsa_status llsa_layer_norm_fwd(const llsa_norm_problem* p, const void* x, const void* weight, const void* bias,
+                                void* y, float* mean, float* rstd, llsa_stream stream);
+
+/* Gradients: with g = dy * weight and xhat = (x - mean) * rstd,
+ *   dx = rstd (g - mean_c(g) - xhat mean_c(g xhat)),
+ *   dweight = sum over rows dy xhat, dbias = sum over rows dy (per batch row
+ * when per_batch).  weight may be NULL as in the forward call; dx, dweight and
+ * dbias are written where not NULL (not all three).  mean, rstd: from the
+ * forward call.  dx may be dy itself with the same strides. */
+llsa_status llsa_layer_norm_bwd(const llsa_norm_problem* p, const void* x, const void* dy, const void* weight,
+                                const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                void* workspace, llsa_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
