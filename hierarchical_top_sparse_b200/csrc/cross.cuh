@@ -71,6 +71,16 @@ cudaError_t launch_row_dot(const Geo& g, const void* o, const void* dO, float* D
 cudaError_t launch_sum_parts(const Geo& g, int parts, const float* part, void* out, const Lay& lay, int heads, int n,
                              cudaStream_t s);
 
+// Tensor-core forward (bf16).  The plan follows from the sizes alone.
+struct TcPlan {
+  int ks, ct, tpi, packed, slices, pairs;
+  int64_t items;
+};
+bool fwd_tc_supported(const Geo& g);
+TcPlan plan_fwd_tc(const Geo& g, int sms);
+cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
+                          const Keys& keys, void* o, float* lse, void* work, cudaStream_t s);
+
 // CUDA-core kernels (fp32 FMA), either type.
 Plan plan_simt(const Geo& g, int sms);
 size_t bwd_work_bytes_simt(const Geo& g, const Plan& p);

@@ -1,0 +1,617 @@
+// k_cross_fwd_tc.cu -- cross attention forward on the 5th-generation tensor
+// cores (tcgen05, accumulators in tensor memory), bf16, d a multiple of 8 up
+// to 128.
+//
+// An item is up to two tiles of 128 query rows of one key head against the
+// key tiles of one split, 128 keys each:
+//   S = Q K^T                     (M = 128 rows, N = the tile's keys, K = d)
+//   one thread per row takes its 128 logits from TMEM, with the running
+//   maximum m and sum l of the softmax, and writes P = 2^(z - m) as bf16 back;
+//   O += P V                      (A = P from TMEM, N = d, K = the tile's keys)
+// The maximum is lazy: O (in TMEM) is rescaled only when a logit exceeds m by
+// more than 2^8, so weights stay below 256.  The bound is the exponential (16
+// a cycle and SM): the two tiles of an item run on warpgroups of their own, so
+// that one tile's products hide behind the other's exponentials.
+//
+// Rows: the tokens of one query head, or, where a head has fewer than 128, the
+// tokens of all heads of a key head, one after the other (each key head's keys
+// are then read once).  Few items are made up for by splitting the keys; the
+// splits' results are fp32 and joined by their LSE.
+//
+// Key tiles that are not whole (the length ends inside, or keys are masked):
+// such keys' logits are replaced, never computed with, and their rows of V are
+// cleared in shared memory, so that 0 * V is 0 whatever V holds.
+//
+// Warps (one CTA per SM, items dealt round robin): 0-3 and 4-7 softmax of tile
+// 0 and 1, 8-11 epilogue, 12 producer (TMA), 13 and 14 MMA issue of tile 0 and
+// 1, 15 clears rows of V; warp 15 also gathers Q where heads are packed.
+// Up to 64 channels, P has columns of its own and S of the next key tile is
+// computed while P of this one is made; above, P takes S's columns.
+#include <math.h>
+
+#include "cross_tc.cuh"
+
+namespace llsa {
+namespace cross {
+namespace fwdtc {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kHeadroom = 8.f;               // log2 of the largest weight before O is rescaled
+constexpr int THREADS = 512;
+constexpr int EPI0 = 8, PRODUCER = 12, MMA0 = 13, FIXER = 15;
+constexpr uint32_t TMEM_COLS = 512;
+
+struct Args {
+  Geo g;
+  Keys keys;
+  Where wq, wk, wv;
+  int ks, ct;                                  // key splits, key tiles per split
+  int tpi;                                     // query tiles per item: 1 or 2
+  int packed;                                  // rows: all heads of a key head
+  int slices, pairs;                           // slices of rows; items' row groups per slice
+  int items;
+  const void* q;                               // where heads are packed
+  void* o;
+  float* lse;
+  FwdWork part;
+  int* err;
+};
+
+template <int NP>
+struct Smem {
+  static constexpr int QST = NP == 1 ? 2 : 1, NS = NP == 1 ? 4 : 2;
+  alignas(1024) unsigned char q[2][QST][NP * kPanel];
+  alignas(1024) unsigned char k[NS][NP * kPanel];
+  alignas(1024) unsigned char v[NS][NP * kPanel];
+  float stat_m[2][128], stat_l[2][128];        // an item's row maxima and sums: softmax -> epilogue
+  alignas(8) uint64_t qfull[2][QST], qempty[2][QST];
+  uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], vready[NS];
+  uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2], st_full[2], drain[2];
+  uint32_t tmem_base;
+};
+static_assert(sizeof(Smem<1>) + 1024 <= 232448 && sizeof(Smem<2>) + 1024 <= 232448, "shared memory of one CTA");
+
+struct Item {
+  int b, hk, h, row0, rows;                    // batch row, key head, query head (not packed), first row, rows of the slice
+  int split, key0, n, len;                     // first key, key tiles, keys of the batch row
+};
+
+__device__ __forceinline__ Item item_of(const Args& a, int it) {
+  Item x;
+  x.split = it % a.ks;
+  const int p = (it / a.ks) % a.pairs, slice = it / a.ks / a.pairs;
+  if (a.packed) {
+    x.b = slice / a.g.hk;
+    x.hk = slice % a.g.hk;
+    x.h = x.hk * a.g.group;
+    x.rows = a.g.group * a.g.nq;
+  } else {
+    x.b = slice / a.g.h;
+    x.h = slice % a.g.h;
+    x.hk = x.h / a.g.group;
+    x.rows = a.g.nq;
+  }
+  x.row0 = p * a.tpi * kTile;
+  x.len = key_count(a.g, a.keys, x.b);
+  const int t0 = x.split * a.ct;
+  const int all = (x.len + kTile - 1) / kTile;
+  const int t1 = min(t0 + a.ct, all);
+  x.n = max(t1 - t0, 0);
+  x.key0 = t0 * kTile;
+  return x;
+}
+__device__ __forceinline__ bool tile_active(const Args& a, const Item& x, int t) {
+  return t < a.tpi && x.row0 + t * kTile < x.rows;
+}
+// Columns of a key tile that are computed: its keys up to the length, rounded up to 32.
+__device__ __forceinline__ int tile_cols(const Item& x, int j) {
+  const int left = x.len - (x.key0 + j * kTile);
+  return left >= kTile ? kTile : (left + 31) & ~31;
+}
+
+// The logits of masked keys become -inf, whatever they are.
+__device__ __forceinline__ void keep_keys(uint32_t r[32], uint32_t bits) {
+  if (bits == 0xffffffffu) return;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!((bits >> i) & 1u)) r[i] = 0xff800000u;
+}
+
+template <int NP>
+__global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constant__ Args a,
+                                                            const __grid_constant__ CUtensorMap tq,
+                                                            const __grid_constant__ CUtensorMap tk,
+                                                            const __grid_constant__ CUtensorMap tv) {
+  using S = Smem<NP>;
+  constexpr int QST = S::QST, NS = S::NS;
+  constexpr uint32_t kBytes = NP * kPanel;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const Geo& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      for (int i = 0; i < QST; ++i) {
+        ptx::mbar_init(&s.qfull[t][i], 1);
+        ptx::mbar_init(&s.qempty[t][i], 1);
+      }
+      ptx::mbar_init(&s.s_full[t], 1);
+      ptx::mbar_init(&s.s_empty[t], 4);
+      ptx::mbar_init(&s.p_full[t], 4);
+      ptx::mbar_init(&s.p_empty[t], 1);
+      ptx::mbar_init(&s.o_full[t], 1);
+      ptx::mbar_init(&s.o_empty[t], 4);
+      ptx::mbar_init(&s.st_full[t], 4);
+      ptx::mbar_init(&s.drain[t], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(&s.kfull[i], 1);
+      ptx::mbar_init(&s.kempty[i], 2);
+      ptx::mbar_init(&s.vfull[i], 1);
+      ptx::mbar_init(&s.vempty[i], 2);
+      ptx::mbar_init(&s.vready[i], 1);
+    }
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(&s.tmem_base, TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = s.tmem_base;
+  // TMEM columns of tile t: S, P (bf16 pairs), O
+  auto col_s = [](int t) { return 128u * t; };
+  auto col_p = [](int t) { return NP == 1 ? 256u + 64u * t : 128u * t; };
+  auto col_o = [](int t) { return NP == 1 ? 384u + 64u * t : 256u + 128u * t; };
+  bool ok = true;
+  // Every lane of a warp waits, and all go on together or all give up together.
+  auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+    if (!ok) return false;
+    ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+    if (!ok && lane == 0) report(a.err, code);
+    return ok;
+  };
+
+  if (warp < 8) {
+    // ============================================================ softmax
+    const int t = warp >> 2, sub = warp & 3;
+    const int row = sub * 32 + lane;
+    const uint32_t tl = tbase + ((uint32_t)(sub * 32) << 16);
+    const float sc2 = g.scale * kLog2e;        // logits in the log2 domain
+    uint32_t sc = 0, oc = 0;
+    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+      const Item x = item_of(a, it);
+      if (!tile_active(a, x, t)) continue;
+      const uint8_t* mask = a.keys.mask ? a.keys.mask + (int64_t)x.b * g.nk : nullptr;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < x.n; ++j, ++sc) {
+        const int key0 = x.key0 + j * kTile;
+        const int blocks = tile_cols(x, j) >> 5;
+        const bool whole = !mask && key0 + kTile <= x.len;
+        uint32_t bits[4];
+        if (!whole) key_bits(mask, key0, x.len, lane, bits);
+        if (!wait(&s.s_full[t], sc & 1, 91)) break;
+        tc::fence_after_sync();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < blocks) {
+            uint32_t r[32];
+            tmem_ld32(tl + col_s(t) + 32u * c, r);
+            tc::tmem_wait_ld();
+            if (!whole) keep_keys(r, bits[c]);
+            float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i & 3] = fmaxf(y[i & 3], __uint_as_float(r[i]));
+            mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+          }
+        const float mn = fmaxf(m, mx * sc2);
+        bool resc = false;
+        float f = 1.f;
+        if (m == -INFINITY) {
+          m = mn;
+        } else if (mn > m + kHeadroom) {
+          resc = true;
+          f = ptx::ex2(m - mn);
+          m = mn;
+          l *= f;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;    // no key so far: every weight is 2^-inf = 0
+        // the O update of the tile before has read P and is in O
+        if (!wait(&s.p_empty[t], (sc & 1) ^ 1, 92)) break;
+        tc::fence_after_sync();
+        if (__any_sync(0xffffffffu, resc)) {
+          const int oc16 = (g.d + 15) >> 4;
+#pragma unroll 1
+          for (int c = 0; c < oc16; ++c) {
+            uint32_t w[16];
+            tc::tmem_ld16(tl + col_o(t) + 16u * c, w);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+            tc::tmem_st16(tl + col_o(t) + 16u * c, w);
+          }
+        }
+        // S once more (it costs less than registers for 128 logits), the next 32 columns on their way
+        float l0 = 0.f, l1 = 0.f;
+        uint32_t r[2][32];
+        tmem_ld32(tl + col_s(t), r[0]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < blocks) {
+            if (c + 1 < blocks) {
+              tmem_ld32(tl + col_s(t) + 32u * (c + 1), r[(c + 1) & 1]);
+            } else if (NP == 1) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(&s.s_empty[t]);
+              __syncwarp();
+            }
+            if (!whole) keep_keys(r[c & 1], bits[c]);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = ptx::ex2(fmaf(__uint_as_float(r[c & 1][2 * i]), sc2, -ref));
+              const float p1 = ptx::ex2(fmaf(__uint_as_float(r[c & 1][2 * i + 1]), sc2, -ref));
+              l0 += p0;
+              l1 += p1;
+              w[i] = ptx::pack_bf16(p0, p1);
+            }
+            tc::tmem_wait_ld();
+            tc::tmem_st16(tl + col_p(t) + 16u * c, w);
+          }
+        l += l0 + l1;
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&s.p_full[t]);
+      }
+      if (!wait(&s.o_empty[t], (oc & 1) ^ 1, 93)) break;    // the epilogue has read the last item's statistics
+      s.stat_m[t][row] = m;
+      s.stat_l[t][row] = l;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&s.st_full[t]);
+      ++oc;
+    }
+  } else {
+    if (warp < EPI0 + 4) {
+      // ============================================================ epilogue
+      const int sub = warp & 3;
+      const uint32_t tl = tbase + ((uint32_t)(sub * 32) << 16);
+      uint32_t oc[2] = {0, 0};
+      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+        const Item x = item_of(a, it);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          if (!tile_active(a, x, t)) continue;
+          const uint32_t c0 = t ? oc[1] : oc[0];
+          if (t) ++oc[1]; else ++oc[0];
+          if (!wait(&s.st_full[t], c0 & 1, 94) || !wait(&s.o_full[t], c0 & 1, 94)) break;
+          tc::fence_after_sync();
+          const float m = s.stat_m[t][sub * 32 + lane], l = s.stat_l[t][sub * 32 + lane];
+          const int r = x.row0 + t * kTile + sub * 32 + lane;
+          const bool live = r < x.rows;
+          int h = x.h, n = r;
+          if (a.packed && live) {
+            h = x.h + r / g.nq;
+            n = r % g.nq;
+          }
+          const bool none = m == -INFINITY && !(l > 0.f) && l == l;    // NaN sums pass through
+          const float inv = none ? 0.f : 1.f / l;
+          const float ls = none ? -INFINITY : (m + log2f(l)) * kLn2;
+          const int64_t at = ((int64_t)x.b * g.h + h) * g.nq + n;
+          __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.o) + x.b * g.o.b + h * g.o.h + n * g.o.n;
+          float* pp = a.part.o + ((int64_t)x.split * rows_of(g) + at) * g.d;
+          const int c16 = (g.d + 15) >> 4;
+#pragma unroll 1
+          for (int c = 0; c < c16; ++c) {
+            uint32_t w[16];
+            tc::tmem_ld16(tl + col_o(t) + 16u * c, w);
+            tc::tmem_wait_ld();
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : __uint_as_float(w[i]) * inv;
+            const bool both = 16 * c + 8 < g.d;
+            if (!live) {
+            } else if (a.ks > 1) {
+              float4* d4 = reinterpret_cast<float4*>(pp + 16 * c);
+              d4[0] = make_float4(f[0], f[1], f[2], f[3]);
+              d4[1] = make_float4(f[4], f[5], f[6], f[7]);
+              if (both) {
+                d4[2] = make_float4(f[8], f[9], f[10], f[11]);
+                d4[3] = make_float4(f[12], f[13], f[14], f[15]);
+              }
+            } else {
+              uint4* d4 = reinterpret_cast<uint4*>(po + 16 * c);
+              d4[0] = make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),
+                                 ptx::pack_bf16(f[6], f[7]));
+              if (both)
+                d4[1] = make_uint4(ptx::pack_bf16(f[8], f[9]), ptx::pack_bf16(f[10], f[11]),
+                                   ptx::pack_bf16(f[12], f[13]), ptx::pack_bf16(f[14], f[15]));
+            }
+            __syncwarp();
+          }
+          if (live) {
+            if (a.ks > 1)
+              a.part.lse[(int64_t)x.split * rows_of(g) + at] = ls;
+            else if (a.lse)
+              a.lse[at] = ls;
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&s.o_empty[t]);
+        }
+      }
+    } else if (warp == PRODUCER) {
+      // ============================================================ producer
+      uint32_t qc[2] = {0, 0}, kc = 0;
+      if (lane == 0) {
+        auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+          if (ok && !ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
+            ok = false;
+            report(a.err, code);
+          }
+          return ok;
+        };
+        for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+          const Item x = item_of(a, it);
+          if (x.n == 0) continue;
+#pragma unroll 1
+          for (int t = 0; t < 2 && !a.packed; ++t) {
+            if (!tile_active(a, x, t)) continue;
+            const uint32_t c = qc[t];
+            uint64_t* full = &s.qfull[t][c % QST];
+            if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 95)) break;
+            ptx::mbar_arrive_expect_tx(full, kBytes);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              tma_load_4d(s.q[t][c % QST] + p * kPanel, &tq, 64 * p, x.row0 + t * kTile, x.h * a.wq.h, x.b * a.wq.b,
+                          full);
+            ++qc[t];
+          }
+          for (int j = 0; j < x.n && ok; ++j) {
+            const uint32_t i = kc % NS, ph = ((kc / NS) & 1) ^ 1;
+            if (!wait(&s.kempty[i], ph, 96)) break;
+            ptx::mbar_arrive_expect_tx(&s.kfull[i], kBytes);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              tma_load_4d(s.k[i] + p * kPanel, &tk, 64 * p, x.key0 + j * kTile, x.hk * a.wk.h, x.b * a.wk.b,
+                          &s.kfull[i]);
+            if (!wait(&s.vempty[i], ph, 96)) break;
+            ptx::mbar_arrive_expect_tx(&s.vfull[i], kBytes);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              tma_load_4d(s.v[i] + p * kPanel, &tv, 64 * p, x.key0 + j * kTile, x.hk * a.wv.h, x.b * a.wv.b,
+                          &s.vfull[i]);
+            ++kc;
+          }
+        }
+        // After a timeout, do not leave while copies issued here may still be landing.
+        if (!ok) {
+          for (int t = 0; t < 2 && !a.packed; ++t)
+            for (uint32_t c = qc[t] > QST ? qc[t] - QST : 0; c < qc[t]; ++c)
+              ptx::mbar_wait_bounded(&s.qfull[t][c % QST], (c / QST) & 1, kWaitLimitNs);
+          for (uint32_t c = kc > NS ? kc - NS : 0; c < kc; ++c) {
+            ptx::mbar_wait_bounded(&s.kfull[c % NS], (c / NS) & 1, kWaitLimitNs);
+            ptx::mbar_wait_bounded(&s.vfull[c % NS], (c / NS) & 1, kWaitLimitNs);
+          }
+          ptx::mbar_wait_bounded(&s.kfull[kc % NS], (kc / NS) & 1, 1000000ull);   // a K without its V
+        }
+      }
+      __syncwarp();
+    } else if (warp == FIXER) {
+      // ============================================================ rows of V; packed queries
+      uint32_t kc = 0, qc[2] = {0, 0};
+      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+        const Item x = item_of(a, it);
+        if (x.n == 0) continue;
+        if (a.packed) {
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            if (!tile_active(a, x, t)) continue;
+            const uint32_t c = qc[t]++;
+            if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 97)) break;
+            unsigned char* dst = s.q[t][c % QST];
+            const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b;
+#pragma unroll 4
+            for (int e = lane; e < kTile * 8 * NP; e += 32) {
+              const int r = e / (8 * NP), ch = e % (8 * NP);
+              const int rr = x.row0 + t * kTile + r;
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              if (rr < x.rows && ch * 8 < g.d)
+                w = *reinterpret_cast<const uint4*>(base + (int64_t)(x.h + rr / g.nq) * g.q.h +
+                                                    (int64_t)(rr % g.nq) * g.q.n + ch * 8);
+              *reinterpret_cast<uint4*>(dst + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
+            }
+            ptx::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.qfull[t][c % QST]);
+          }
+          if (!ok) break;
+        }
+        const uint8_t* mask = a.keys.mask ? a.keys.mask + (int64_t)x.b * g.nk : nullptr;
+        for (int j = 0; j < x.n; ++j, ++kc) {
+          const int key0 = x.key0 + j * kTile;
+          const uint32_t i = kc % NS;
+          const bool whole = !mask && key0 + kTile <= x.len;
+          uint32_t bits[4];
+          if (!whole) key_bits(mask, key0, x.len, lane, bits);
+          if (!wait(&s.vfull[i], (kc / NS) & 1, 98)) break;
+          if (!whole) {
+            clear_rows<NP>(s.v[i], bits, lane);
+            ptx::fence_proxy_async();
+            __syncwarp();
+          }
+          if (lane == 0) ptx::mbar_arrive(&s.vready[i]);
+        }
+      }
+    } else {
+      // ============================================================ MMA issue of tile t
+      const int t = warp - MMA0;
+      const uint64_t dk0 = tc::sw128_desc(ptx::smem_u32(s.k[0]), 16, 1024);
+      const uint64_t dv0 = tc::sw128_desc(ptx::smem_u32(s.v[0]), kPanel, 1024);
+      const uint64_t dq0 = tc::sw128_desc(ptx::smem_u32(s.q[t][0]), 16, 1024);
+      const int dsteps = (g.d + 15) >> 4;
+      const uint32_t id_o = tc::idesc_bf16(128, 16 * dsteps, 0, 1);      // O += P V: A = P (TMEM), B = V (MN-major)
+      uint32_t kc = 0, sc = 0, qc = 0, oc = 0;
+      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+        const Item x = item_of(a, it);
+        if (!tile_active(a, x, t)) {           // the other tile's keys pass by
+          for (int j = 0; j < x.n && ok; ++j, ++kc) {
+            const uint32_t i = kc % NS, ph = (kc / NS) & 1;
+            if (!wait(&s.kfull[i], ph, 99)) break;
+            if (lane == 0) ptx::mbar_arrive(&s.kempty[i]);
+            if (!wait(&s.vready[i], ph, 99)) break;
+            if (lane == 0) ptx::mbar_arrive(&s.vempty[i]);
+          }
+          continue;
+        }
+        auto issue_s = [&](int j) {
+          const uint32_t c = kc + j, i = c % NS;
+          if (!wait(&s.kfull[i], (c / NS) & 1, 99)) return;
+          // NP == 1: the softmax has read the last S; NP == 2: the O update has read P from these columns
+          if (!wait(NP == 1 ? &s.s_empty[t] : &s.p_empty[t], ((sc + j) & 1) ^ 1, 99)) return;
+          tc::fence_after_sync();
+          const uint32_t id = tc::idesc_bf16(128, tile_cols(x, j), 0, 0);
+          const uint64_t qd = dq0 + (uint64_t)(qc % QST) * (kBytes >> 4), kd = dk0 + (uint64_t)i * (kBytes >> 4);
+          if (tc::elect_one()) {
+            for (int k = 0; k < dsteps; ++k) {
+              const uint64_t o = (uint64_t)(k >> 2) * (kPanel >> 4) + 2u * (k & 3);
+              tc::mma_bf16(tbase + col_s(t), qd + o, kd + o, id, k > 0);
+            }
+            tc::commit(&s.s_full[t]);
+            tc::commit(&s.kempty[i]);
+            if (j == x.n - 1) tc::commit(&s.qempty[t][qc % QST]);
+          }
+          __syncwarp();
+        };
+        auto issue_o = [&](int j) {
+          const uint32_t c = kc + j, i = c % NS;
+          if (!wait(&s.vready[i], (c / NS) & 1, 99)) return;
+          if (!wait(&s.p_full[t], (sc + j) & 1, 99)) return;
+          if (j == 0 && !wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) return;    // the last item's O has been read
+          tc::fence_after_sync();
+          const int steps = (tile_cols(x, j)) >> 4;
+          const uint64_t vd = dv0 + (uint64_t)i * (kBytes >> 4);
+          if (tc::elect_one()) {
+            for (int k = 0; k < steps; ++k)    // 16 keys: 8 columns of P, 2 KB of V's panel
+              tc::mma_bf16_ta(tbase + col_o(t), tbase + col_p(t) + 8u * k, vd + 128u * k, id_o, j > 0 || k > 0);
+            tc::commit(&s.p_empty[t]);
+            tc::commit(&s.vempty[i]);
+          }
+          __syncwarp();
+        };
+        if (x.n > 0) {
+          if (!wait(&s.qfull[t][qc % QST], (qc / QST) & 1, 99)) break;
+          issue_s(0);
+          for (int j = 0; j < x.n && ok; ++j) {
+            if (NP == 1 && j + 1 < x.n) issue_s(j + 1);
+            if (ok) issue_o(j);
+            if (NP == 2 && ok && j + 1 < x.n) issue_s(j + 1);
+          }
+          kc += x.n;
+          sc += x.n;
+          ++qc;
+        } else if (!wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) {
+          break;
+        }
+        if (!ok) break;
+        if (tc::elect_one()) tc::commit(&s.o_full[t]);
+        __syncwarp();
+        ++oc;
+      }
+      // every MMA issued here has finished before TMEM is released
+      if (tc::elect_one()) tc::commit(&s.drain[t]);
+      __syncwarp();
+      ptx::mbar_wait_bounded(&s.drain[t], 0, kWaitLimitNs);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, TMEM_COLS);
+  }
+}
+
+}  // namespace fwdtc
+
+bool fwd_tc_supported(const Geo& g) {
+  return g.bf16 && tokens_apart(g.q, g.nq) && tokens_apart(g.k, g.nk) && tokens_apart(g.v, g.nk);
+}
+
+// Items: two query tiles each where that still fills the device; the keys are
+// split (whole tiles, as even as they come) when there are fewer items than
+// SMs, into four times as many as SMs at most, so that rows of unlike length
+// even out.
+TcPlan plan_fwd_tc(const Geo& g, int sms) {
+  TcPlan p;
+  p.packed = g.group > 1 && g.nq < kTile;
+  p.slices = p.packed ? g.b * g.hk : g.b * g.h;
+  const int64_t rows = p.packed ? (int64_t)g.group * g.nq : g.nq;
+  const int64_t tiles = (rows + kTile - 1) / kTile;
+  p.tpi = tiles > 1 && p.slices * ((tiles + 1) / 2) >= sms ? 2 : 1;
+  p.pairs = (int)((tiles + p.tpi - 1) / p.tpi);
+  const int64_t items = (int64_t)p.slices * p.pairs;
+  const int64_t nkt = (g.nk + kTile - 1) / kTile;
+  int64_t ks = 1;
+  if (items < sms && nkt >= 4) {
+    ks = (4 * sms + items - 1) / items;
+    if (ks > nkt / 2) ks = nkt / 2;
+    if (ks > 64) ks = 64;
+  }
+  p.ct = (int)((nkt + ks - 1) / ks);
+  p.ks = (int)((nkt + p.ct - 1) / p.ct);
+  p.items = items * p.ks;
+  return p;
+}
+
+template <int NP>
+static cudaError_t launch(const fwdtc::Args& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int grid, cudaStream_t s) {
+  const size_t smem = sizeof(fwdtc::Smem<NP>) + 1024;
+  cudaError_t e =
+      cudaFuncSetAttribute(fwdtc::fwd_tc_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  fwdtc::fwd_tc_kernel<NP><<<grid, fwdtc::THREADS, smem, s>>>(a, tq, tk, tv);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
+                          const Keys& keys, void* o, float* lse, void* work, cudaStream_t s) {
+  fwdtc::Args a;
+  CUtensorMap tq, tk, tv;
+  cudaError_t e = make_map4(&tq, &a.wq, q, g.q, g.h, g.b, g.nq, g.d, kTile);
+  if (e == cudaSuccess) e = make_map4(&tk, &a.wk, k, g.k, g.hk, g.b, g.nk, g.d, kTile);
+  if (e == cudaSuccess) e = make_map4(&tv, &a.wv, v, g.v, g.hk, g.b, g.nk, g.d, kTile);
+  if (e != cudaSuccess) return e;
+  a.g = g;
+  a.keys = keys;
+  a.q = q;
+  a.ks = p.ks;
+  a.ct = p.ct;
+  a.tpi = p.tpi;
+  a.packed = p.packed;
+  a.slices = p.slices;
+  a.pairs = p.pairs;
+  a.items = (int)p.items;
+  a.o = o;
+  a.lse = lse;
+  a.part = carve_fwd(g, p.ks, work);
+  a.err = device_error_word();
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = a.items < sms ? a.items : sms;
+  e = g.d <= 64 ? launch<1>(a, tq, tk, tv, grid, s) : launch<2>(a, tq, tk, tv, grid, s);
+  if (e == cudaSuccess && p.ks > 1) e = launch_join_fwd(g, p.ks, a.part, o, lse, s);
+  return e;
+}
+
+}  // namespace cross
+}  // namespace llsa

@@ -229,7 +229,9 @@ __global__ void join_fwd_kernel(const __grid_constant__ Geo g, int ks, FwdWork p
     float sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < ks; ++s) {
-      const float w = exp2f((part.lse[s * rows + r] - ref) * kLog2e);
+      const float ls = part.lse[s * rows + r];
+      if (ls == -INFINITY) continue;                     // a split without keys has written no O
+      const float w = exp2f((ls - ref) * kLog2e);
       const float4 y = load4(part.o + (s * rows + r) * g.d + c);
       sum += w;
       x.x = fmaf(w, y.x, x.x);

@@ -227,6 +227,10 @@ llsa_status llsa_cross_query_sizes(const llsa_cross_problem* p, llsa_cross_buffe
   const llsa::cross::Plan plan = llsa::cross::plan_simt(g, llsa::kSms);
   out->lse_bytes = (size_t)llsa::cross::rows_of(g) * sizeof(float);
   out->fwd_workspace_bytes = llsa::cross::fwd_work_bytes(g, plan.fwd_ks);
+  if (g.bf16) {                                 // the strides decide which kernel runs
+    const size_t tc = llsa::cross::fwd_work_bytes(g, llsa::cross::plan_fwd_tc(g, llsa::kSms).ks);
+    if (tc > out->fwd_workspace_bytes) out->fwd_workspace_bytes = tc;
+  }
   out->bwd_workspace_bytes = llsa::cross::bwd_work_bytes_simt(g, plan);
   return LLSA_OK;
 }
@@ -241,9 +245,14 @@ llsa_status llsa_cross_attn_fwd(const llsa_cross_problem* p, const void* q, cons
   LLSA_NEED(o);
   LLSA_MAY(kv_len, 4);
   LLSA_MAY(lse, 16);
-  const llsa::cross::Plan plan = llsa::cross::plan_simt(g, llsa::kSms);
-  if (llsa::cross::fwd_work_bytes(g, plan.fwd_ks)) LLSA_NEED(workspace);
   const llsa::cross::Keys keys{kv_len, key_mask};
+  if (llsa::cross::fwd_tc_supported(g)) {
+    const llsa::cross::TcPlan plan = llsa::cross::plan_fwd_tc(g, llsa::kSms);
+    if (plan.ks > 1) LLSA_NEED(workspace);
+    return llsa::launched(llsa::cross::launch_fwd_tc(g, plan, q, k, v, keys, o, lse, workspace, (cudaStream_t)stream));
+  }
+  const llsa::cross::Plan plan = llsa::cross::plan_simt(g, llsa::kSms);
+  if (plan.fwd_ks > 1) LLSA_NEED(workspace);
   return llsa::launched(llsa::cross::launch_fwd_simt(g, plan, q, k, v, keys, o, lse, workspace, (cudaStream_t)stream));
 }
 
@@ -270,7 +279,7 @@ llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, cons
 
 llsa_status llsa_cross_attn_paths(const llsa_cross_problem* p, int* fwd_tc, int* bwd_tc) {
   LLSA_CROSS(p, g);
-  if (fwd_tc) *fwd_tc = 0;
+  if (fwd_tc) *fwd_tc = llsa::cross::fwd_tc_supported(g);
   if (bwd_tc) *bwd_tc = 0;
   return LLSA_OK;
 }

@@ -108,6 +108,15 @@ def test_masks(dtype, fill, nq, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 72, 128])
+@pytest.mark.parametrize("b,h,hk,nq,nk", [(2, 80, 80, 300, 130), (3, 64, 16, 129, 70), (2, 160, 4, 100, 300),
+                                          (4, 50, 50, 257, 400)])
+def test_many_heads(b, h, hk, nq, nk, d):
+    """Enough tiles to fill the device several times over, with lengths that leave some of them nothing."""
+    run_case(BF16, b, h, hk, nq, nk, d, layout="bnhd", lens=[nk, nk // 2, 0, 1][:b])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("sharp,scale", [(20.0, None), (1.0, 3.0), (1.0, 1e-4)])
 def test_sharp_and_flat_softmax(dtype, sharp, scale):
