@@ -68,8 +68,9 @@ inline FwdWork carve_fwd(const Geo& g, int ks, void* work) {
 // Joins the key splits of the forward; sums the splits of a gradient.
 cudaError_t launch_join_fwd(const Geo& g, int ks, const FwdWork& w, void* o, float* lse, cudaStream_t s);
 cudaError_t launch_row_dot(const Geo& g, const void* o, const void* dO, float* D, cudaStream_t s);
-cudaError_t launch_sum_parts(const Geo& g, int parts, const float* part, void* out, const Lay& lay, int heads, int n,
-                             cudaStream_t s);
+cudaError_t launch_sum_q(const Geo& g, int parts, const float* part, void* dq, cudaStream_t s);
+cudaError_t launch_sum_kv(const Geo& g, int parts, const float* partk, const float* partv, void* dk, void* dv,
+                          cudaStream_t s);
 
 // Tensor-core forward (bf16).  The plan follows from the sizes alone.
 struct TcPlan {
@@ -80,6 +81,18 @@ bool fwd_tc_supported(const Geo& g);
 TcPlan plan_fwd_tc(const Geo& g, int sms);
 cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
                           const Keys& keys, void* o, float* lse, void* work, cudaStream_t s);
+
+// Tensor-core backward where all keys fit one tile (bf16, nk <= 128).
+struct OnePlan {
+  int packed, qs, nqt, units;
+  int64_t items;
+};
+bool bwd_one_supported(const Geo& g);
+OnePlan plan_bwd_one(const Geo& g, int sms);
+size_t bwd_one_work_bytes(const Geo& g, const OnePlan& p);
+cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const void* q, const void* k, const void* v,
+                           const Keys& keys, const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                           void* work, cudaStream_t s);
 
 // CUDA-core kernels (fp32 FMA), either type.
 Plan plan_simt(const Geo& g, int sms);

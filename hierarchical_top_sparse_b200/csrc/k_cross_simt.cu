@@ -498,17 +498,26 @@ __global__ void __launch_bounds__(THREADS) dkv_kernel(const __grid_constant__ Ge
   }
 }
 
-// out = sum of the parts, in order; one thread per four channels.
+// out = sum of the parts, in order; one thread per four channels; the second
+// row of the grid takes the second tensor.
+struct Sums {
+  const float* part[2];
+  void* out[2];
+  Lay lay[2];
+};
 template <typename T>
-__global__ void sum_parts_kernel(int parts, const float* __restrict__ part, T* __restrict__ out, Lay lay, int heads,
-                                 int n, int d, int64_t rows) {
+__global__ void sum_parts_kernel(int parts, const __grid_constant__ Sums a, int heads, int n, int d, int64_t rows) {
   const int c4 = d / 4;
   const int64_t total = rows * c4;
+  const int which = blockIdx.y;
+  const float* part = a.part[which];
+  T* out = static_cast<T*>(a.out[which]);
+  const Lay lay = a.lay[which];
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t r = i / c4;
     const int c = (int)(i % c4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < parts; ++s) {
       const float4 y = load4(part + (s * rows + r) * d + c);
       x.x += y.x;
@@ -548,16 +557,24 @@ cudaError_t launch_row_dot(const Geo& g, const void* o, const void* dO, float* D
   return cudaGetLastError();
 }
 
-cudaError_t launch_sum_parts(const Geo& g, int parts, const float* part, void* out, const Lay& lay, int heads, int n,
-                             cudaStream_t s) {
+static cudaError_t sum_parts(const Geo& g, int parts, const Sums& a, int tensors, int heads, int n, cudaStream_t s) {
   const int64_t rows = (int64_t)g.b * heads * n;
-  const int grid = grid_for(rows * (g.d / 4), 128);
+  const dim3 grid((unsigned)grid_for(rows * (g.d / 4), 128), (unsigned)tensors);
   if (g.bf16)
-    sum_parts_kernel<<<grid, 128, 0, s>>>(parts, part, (__nv_bfloat16*)out, lay, heads, n, g.d, rows);
+    sum_parts_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(parts, a, heads, n, g.d, rows);
   else
-    sum_parts_kernel<<<grid, 128, 0, s>>>(parts, part, (float*)out, lay, heads, n, g.d, rows);
+    sum_parts_kernel<float><<<grid, 128, 0, s>>>(parts, a, heads, n, g.d, rows);
   note_launches(1);
   return cudaGetLastError();
+}
+
+cudaError_t launch_sum_q(const Geo& g, int parts, const float* part, void* dq, cudaStream_t s) {
+  return sum_parts(g, parts, Sums{{part, nullptr}, {dq, nullptr}, {g.dq, Lay{}}}, 1, g.h, g.nq, s);
+}
+
+cudaError_t launch_sum_kv(const Geo& g, int parts, const float* partk, const float* partv, void* dk, void* dv,
+                          cudaStream_t s) {
+  return sum_parts(g, parts, Sums{{partk, partv}, {dk, dv}, {g.dk, g.dv}}, 2, g.hk, g.nk, s);
 }
 
 // Splits fill the device once or twice over when the tiles alone do not: at
@@ -647,17 +664,14 @@ static cudaError_t bwd(const Geo& g, const Plan& p, const void* q, const void* k
                                                                     (const T*)v, (const T*)dO, lse, w.D, (T*)dq, w.dq);
   note_launches(1);
   e = cudaGetLastError();
-  if (e == cudaSuccess && p.dq_ks > 1) e = launch_sum_parts(g, p.dq_ks, w.dq, dq, g.dq, g.h, g.nq, s);
+  if (e == cudaSuccess && p.dq_ks > 1) e = launch_sum_q(g, p.dq_ks, w.dq, dq, s);
   if (e != cudaSuccess) return e;
   const int64_t gk = (int64_t)g.b * g.hk * ((g.nk + BN - 1) / BN) * p.dkv_qs;
   dkv_kernel<T, DP><<<(unsigned)gk, THREADS, sizeof(DkvSmem<DP>), s>>>(
       g, keys, p.dkv_qs, (const T*)q, (const T*)k, (const T*)v, (const T*)dO, lse, w.D, (T*)dk, (T*)dv, w.dk, w.dv);
   note_launches(1);
   e = cudaGetLastError();
-  if (e == cudaSuccess && p.dkv_qs > 1) {
-    e = launch_sum_parts(g, p.dkv_qs, w.dk, dk, g.dk, g.hk, g.nk, s);
-    if (e == cudaSuccess) e = launch_sum_parts(g, p.dkv_qs, w.dv, dv, g.dv, g.hk, g.nk, s);
-  }
+  if (e == cudaSuccess && p.dkv_qs > 1) e = launch_sum_kv(g, p.dkv_qs, w.dk, w.dv, dk, dv, s);
   return e;
 }
 
