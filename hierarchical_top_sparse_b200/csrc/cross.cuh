@@ -82,17 +82,12 @@ TcPlan plan_fwd_tc(const Geo& g, int sms);
 cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
                           const Keys& keys, void* o, float* lse, void* work, cudaStream_t s);
 
-// Tensor-core backward where all keys fit one tile (bf16, nk <= 128).
-struct OnePlan {
-  int packed, qs, nqt, units;
-  int64_t items;
-};
-bool bwd_one_supported(const Geo& g);
-OnePlan plan_bwd_one(const Geo& g, int sms);
-size_t bwd_one_work_bytes(const Geo& g, const OnePlan& p);
-cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const void* q, const void* k, const void* v,
-                           const Keys& keys, const void* dO, const float* lse, void* dq, void* dk, void* dv,
-                           void* work, cudaStream_t s);
+// Tensor-core backward (bf16).
+bool bwd_tc_supported(const Geo& g);
+size_t bwd_work_bytes_tc(const Geo& g, int sms);
+cudaError_t launch_bwd_tc(const Geo& g, int sms, const void* q, const void* k, const void* v, const Keys& keys,
+                          const void* o, const void* dO, const float* lse, void* dq, void* dk, void* dv, void* work,
+                          cudaStream_t s);
 
 // CUDA-core kernels (fp32 FMA), either type.
 Plan plan_simt(const Geo& g, int sms);

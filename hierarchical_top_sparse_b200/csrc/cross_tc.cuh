@@ -89,5 +89,78 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, const uint32_t b
   }
 }
 
+// Gathers the 128 rows that at(r, head, token) names (zeros where it says
+// false) from a batch row at `base` into a swizzled tile (every lane of a warp).
+template <int PANELS, typename At>
+__device__ __forceinline__ void gather_rows(unsigned char* tile, const __nv_bfloat16* base, const Lay& lay, int d,
+                                            int lane, At at) {
+#pragma unroll 4
+  for (int e = lane; e < kTile * 8 * PANELS; e += 32) {
+    const int r = e / (8 * PANELS), ch = e % (8 * PANELS);
+    int h, n;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (at(r, h, n) && ch * 8 < d) w = *reinterpret_cast<const uint4*>(base + h * lay.h + n * lay.n + ch * 8);
+    *reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
+  }
+}
+
+// 16 channels (8 unless `both`) as bf16 to `out`, or, where that is null, as fp32 to `part`.
+__device__ __forceinline__ void store16(const float* f, __nv_bfloat16* out, float* part, bool both) {
+  if (out) {
+    uint4* d4 = reinterpret_cast<uint4*>(out);
+    d4[0] = make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),
+                       ptx::pack_bf16(f[6], f[7]));
+    if (both)
+      d4[1] = make_uint4(ptx::pack_bf16(f[8], f[9]), ptx::pack_bf16(f[10], f[11]), ptx::pack_bf16(f[12], f[13]),
+                         ptx::pack_bf16(f[14], f[15]));
+  } else {
+    float4* d4 = reinterpret_cast<float4*>(part);
+    d4[0] = make_float4(f[0], f[1], f[2], f[3]);
+    d4[1] = make_float4(f[4], f[5], f[6], f[7]);
+    if (both) {
+      d4[2] = make_float4(f[8], f[9], f[10], f[11]);
+      d4[3] = make_float4(f[12], f[13], f[14], f[15]);
+    }
+  }
+}
+
+inline int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+int splits_of_queries(int64_t slices, int units, int sms);
+
+// The backward where all keys fit one tile (nk <= 128).
+struct OnePlan {
+  int packed, qs, nqt, units;
+  int64_t items;
+};
+OnePlan plan_bwd_one(const Geo& g, int sms);
+cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const CUtensorMap* t, const Where* w, const void* q,
+                           const Keys& keys, const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                           float* partk, float* partv, cudaStream_t s);
+
+// The parts of the backward for more than one tile of keys.  t, w: maps of q,
+// k, v, dO with boxes of 128 tokens.
+struct DqPlan {
+  int packed, ks, ct, tiles;
+  int64_t items;
+};
+DqPlan plan_bwd_q(const Geo& g, int sms);
+cudaError_t launch_bwd_q(const Geo& g, const DqPlan& p, const CUtensorMap* t, const Where* w, const void* q,
+                         const Keys& keys, const void* dO, const float* lse, const float* D, void* dq, float* part,
+                         cudaStream_t s);
+struct DkvPlan {
+  int packed, qs, nqt, units, tiles;
+  int64_t items;
+};
+DkvPlan plan_bwd_kv(const Geo& g, int sms);
+cudaError_t launch_bwd_kv(const Geo& g, const DkvPlan& p, const CUtensorMap* t, const Where* w, const void* q,
+                          const Keys& keys, const void* dO, const float* lse, const float* D, void* dk, void* dv,
+                          float* partk, float* partv, cudaStream_t s);
+
 }  // namespace cross
 }  // namespace llsa

@@ -270,25 +270,7 @@ bwd_one_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
       float v[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = none || !keep ? 0.f : __uint_as_float(w[e]) * f;
-      const bool both = 16 * c + 8 < g.d;
-      if (live) {
-        if (part) {
-          float4* d4 = reinterpret_cast<float4*>(part + 16 * c);
-          d4[0] = make_float4(v[0], v[1], v[2], v[3]);
-          d4[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (both) {
-            d4[2] = make_float4(v[8], v[9], v[10], v[11]);
-            d4[3] = make_float4(v[12], v[13], v[14], v[15]);
-          }
-        } else {
-          uint4* d4 = reinterpret_cast<uint4*>(out + 16 * c);
-          d4[0] = make_uint4(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]), ptx::pack_bf16(v[4], v[5]),
-                             ptx::pack_bf16(v[6], v[7]));
-          if (both)
-            d4[1] = make_uint4(ptx::pack_bf16(v[8], v[9]), ptx::pack_bf16(v[10], v[11]),
-                               ptx::pack_bf16(v[12], v[13]), ptx::pack_bf16(v[14], v[15]));
-        }
-      }
+      if (live) store16(v, part ? nullptr : out + 16 * c, part + 16 * c, 16 * c + 8 < g.d);
       __syncwarp();
     };
     for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
@@ -394,21 +376,9 @@ bwd_one_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
       for (int i = 0; i < x.n && a.packed; ++i, ++tc_) {
         const uint32_t st = tc_ % ST;
         if (!wait(&s.empty[st], ((tc_ / ST) & 1) ^ 1, 109)) break;
-        const __nv_bfloat16* bq = static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b;
-        const __nv_bfloat16* bg = static_cast<const __nv_bfloat16*>(a.dO) + x.b * g.dO.b;
-#pragma unroll 2
-        for (int e = lane; e < kTile * 8 * NP; e += 32) {
-          const int r = e / (8 * NP), ch = e % (8 * NP);
-          int h, n;
-          uint4 wq = make_uint4(0u, 0u, 0u, 0u), wg = wq;
-          if (row_of(a, x.hk, x.u0 + i, r, h, n) && ch * 8 < g.d) {
-            wq = *reinterpret_cast<const uint4*>(bq + h * g.q.h + n * g.q.n + ch * 8);
-            wg = *reinterpret_cast<const uint4*>(bg + h * g.dO.h + n * g.dO.n + ch * 8);
-          }
-          const int to = (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(s.q[st] + to) = wq;
-          *reinterpret_cast<uint4*>(s.dO[st] + to) = wg;
-        }
+        auto at = [&](int r, int& h, int& n) { return row_of(a, x.hk, x.u0 + i, r, h, n); };
+        gather_rows<NP>(s.q[st], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane, at);
+        gather_rows<NP>(s.dO[st], static_cast<const __nv_bfloat16*>(a.dO) + x.b * g.dO.b, g.dO, g.d, lane, at);
         ptx::fence_proxy_async();
         arrive(&s.full[st]);
       }
@@ -525,37 +495,33 @@ bwd_one_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
 
 }  // namespace bwdone
 
-bool bwd_one_supported(const Geo& g) {
-  return g.bf16 && g.nk <= kTile && tokens_apart(g.q, g.nq) && tokens_apart(g.k, g.nk) && tokens_apart(g.v, g.nk) &&
-         tokens_apart(g.dO, g.nq);
+// The number of splits that needs the fewest tiles one after the other on an
+// SM.  A run of tiles costs about two tiles more (filling, storing the
+// accumulators), and a split's partial sums about an eighth of a tile.
+int splits_of_queries(int64_t slices, int units, int sms) {
+  double best = 0;
+  int splits = 1;
+  for (int qs = 1; qs <= sms && qs <= units; ++qs) {
+    const int64_t waves = (slices * qs + sms - 1) / sms;
+    const double cost =
+        (double)waves * ((units + qs - 1) / qs + 2) + (qs > 1 ? 2.0 + 0.125 * qs * (double)slices / sms : 0.0);
+    if (qs == 1 || cost < best) {
+      best = cost;
+      splits = qs;
+    }
+  }
+  return splits;
 }
 
-// Query splits: the number that needs the fewest tiles one after the other on
-// an SM, each split beyond the first counting for the partial sums it leaves
-// (about an eighth of a tile).
 OnePlan plan_bwd_one(const Geo& g, int sms) {
   OnePlan p;
   p.packed = g.group > 1 && g.nq < kTile;
   p.nqt = (g.nq + kTile - 1) / kTile;
   p.units = (int)(p.packed ? ((int64_t)g.group * g.nq + kTile - 1) / kTile : (int64_t)g.group * p.nqt);
   const int64_t slices = (int64_t)g.b * g.hk;
-  double best = 0;
-  p.qs = 1;
-  for (int qs = 1; qs <= 148 && qs <= p.units; ++qs) {
-    const int64_t waves = (slices * qs + sms - 1) / sms;
-    // a run of tiles costs about two tiles more (filling, the accumulators' store)
-    const double cost = (double)waves * ((p.units + qs - 1) / qs + 2) + (qs > 1 ? 2.0 + 0.125 * qs * slices / sms : 0.0);
-    if (qs == 1 || cost < best) {
-      best = cost;
-      p.qs = qs;
-    }
-  }
+  p.qs = splits_of_queries(slices, p.units, sms);
   p.items = slices * p.qs;
   return p;
-}
-
-size_t bwd_one_work_bytes(const Geo& g, const OnePlan& p) {
-  return p.qs > 1 ? 2 * round256((size_t)p.qs * keys_of(g) * g.d * 4) : 0;
 }
 
 template <int NP>
@@ -569,18 +535,16 @@ static cudaError_t launch(const bwdone::Args& a, const CUtensorMap* t, int grid,
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const void* q, const void* k, const void* v,
+cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const CUtensorMap* t, const Where* w, const void* q,
                            const Keys& keys, const void* dO, const float* lse, void* dq, void* dk, void* dv,
-                           void* work, cudaStream_t s) {
+                           float* partk, float* partv, cudaStream_t s) {
   bwdone::Args a;
-  CUtensorMap t[4];
-  cudaError_t e = make_map4(&t[0], &a.wq, q, g.q, g.h, g.b, g.nq, g.d, kTile);
-  if (e == cudaSuccess) e = make_map4(&t[1], &a.wk, k, g.k, g.hk, g.b, g.nk, g.d, kTile);
-  if (e == cudaSuccess) e = make_map4(&t[2], &a.wv, v, g.v, g.hk, g.b, g.nk, g.d, kTile);
-  if (e == cudaSuccess) e = make_map4(&t[3], &a.wg, dO, g.dO, g.h, g.b, g.nq, g.d, kTile);
-  if (e != cudaSuccess) return e;
   a.g = g;
   a.keys = keys;
+  a.wq = w[0];
+  a.wk = w[1];
+  a.wv = w[2];
+  a.wg = w[3];
   a.packed = p.packed;
   a.qs = p.qs;
   a.nqt = p.nqt;
@@ -592,16 +556,14 @@ cudaError_t launch_bwd_one(const Geo& g, const OnePlan& p, const void* q, const 
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.partk = static_cast<float*>(work);
-  a.partv = reinterpret_cast<float*>(static_cast<char*>(work) + round256((size_t)p.qs * keys_of(g) * g.d * 4));
+  a.partk = partk;
+  a.partv = partv;
   a.err = device_error_word();
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   const int grid = a.items < sms ? a.items : sms;
-  e = g.d <= 64 ? launch<1>(a, t, grid, s) : launch<2>(a, t, grid, s);
-  if (e == cudaSuccess && p.qs > 1) e = launch_sum_kv(g, p.qs, a.partk, a.partv, dk, dv, s);
-  return e;
+  const cudaError_t e = g.d <= 64 ? launch<1>(a, t, grid, s) : launch<2>(a, t, grid, s);
+  if (e != cudaSuccess || p.qs == 1) return e;
+  return launch_sum_kv(g, p.qs, partk, partv, dk, dv, s);
 }
 
 }  // namespace cross

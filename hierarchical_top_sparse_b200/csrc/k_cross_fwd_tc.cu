@@ -315,24 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
             float f[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : __uint_as_float(w[i]) * inv;
-            const bool both = 16 * c + 8 < g.d;
-            if (!live) {
-            } else if (a.ks > 1) {
-              float4* d4 = reinterpret_cast<float4*>(pp + 16 * c);
-              d4[0] = make_float4(f[0], f[1], f[2], f[3]);
-              d4[1] = make_float4(f[4], f[5], f[6], f[7]);
-              if (both) {
-                d4[2] = make_float4(f[8], f[9], f[10], f[11]);
-                d4[3] = make_float4(f[12], f[13], f[14], f[15]);
-              }
-            } else {
-              uint4* d4 = reinterpret_cast<uint4*>(po + 16 * c);
-              d4[0] = make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),
-                                 ptx::pack_bf16(f[6], f[7]));
-              if (both)
-                d4[1] = make_uint4(ptx::pack_bf16(f[8], f[9]), ptx::pack_bf16(f[10], f[11]),
-                                   ptx::pack_bf16(f[12], f[13]), ptx::pack_bf16(f[14], f[15]));
-            }
+            if (live) store16(f, a.ks > 1 ? nullptr : po + 16 * c, pp + 16 * c, 16 * c + 8 < g.d);
             __syncwarp();
           }
           if (live) {
@@ -415,18 +398,13 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
             if (!tile_active(a, x, t)) continue;
             const uint32_t c = qc[t]++;
             if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 97)) break;
-            unsigned char* dst = s.q[t][c % QST];
-            const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b;
-#pragma unroll 4
-            for (int e = lane; e < kTile * 8 * NP; e += 32) {
-              const int r = e / (8 * NP), ch = e % (8 * NP);
-              const int rr = x.row0 + t * kTile + r;
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              if (rr < x.rows && ch * 8 < g.d)
-                w = *reinterpret_cast<const uint4*>(base + (int64_t)(x.h + rr / g.nq) * g.q.h +
-                                                    (int64_t)(rr % g.nq) * g.q.n + ch * 8);
-              *reinterpret_cast<uint4*>(dst + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
-            }
+            gather_rows<NP>(s.q[t][c % QST], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane,
+                            [&](int r, int& h, int& n) {
+                              const int rr = x.row0 + t * kTile + r;
+                              h = x.h + rr / g.nq;
+                              n = rr % g.nq;
+                              return rr < x.rows;
+                            });
             ptx::fence_proxy_async();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.qfull[t][c % QST]);
@@ -604,9 +582,7 @@ cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const vo
   a.lse = lse;
   a.part = carve_fwd(g, p.ks, work);
   a.err = device_error_word();
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   const int grid = a.items < sms ? a.items : sms;
   e = g.d <= 64 ? launch<1>(a, tq, tk, tv, grid, s) : launch<2>(a, tq, tk, tv, grid, s);
   if (e == cudaSuccess && p.ks > 1) e = launch_join_fwd(g, p.ks, a.part, o, lse, s);

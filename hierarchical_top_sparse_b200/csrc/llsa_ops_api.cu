@@ -227,13 +227,13 @@ llsa_status llsa_cross_query_sizes(const llsa_cross_problem* p, llsa_cross_buffe
   const llsa::cross::Plan plan = llsa::cross::plan_simt(g, llsa::kSms);
   out->lse_bytes = (size_t)llsa::cross::rows_of(g) * sizeof(float);
   out->fwd_workspace_bytes = llsa::cross::fwd_work_bytes(g, plan.fwd_ks);
-  if (g.bf16) {                                 // the strides decide which kernel runs
+  out->bwd_workspace_bytes = llsa::cross::bwd_work_bytes_simt(g, plan);
+  if (g.bf16) {                                 // the strides decide which kernels run: room for either
     const size_t tc = llsa::cross::fwd_work_bytes(g, llsa::cross::plan_fwd_tc(g, llsa::kSms).ks);
     if (tc > out->fwd_workspace_bytes) out->fwd_workspace_bytes = tc;
-    const size_t one = g.nk <= 128 ? llsa::cross::bwd_one_work_bytes(g, llsa::cross::plan_bwd_one(g, llsa::kSms)) : 0;
-    if (one > out->bwd_workspace_bytes) out->bwd_workspace_bytes = one;
+    const size_t bwd = llsa::cross::bwd_work_bytes_tc(g, llsa::kSms);
+    if (bwd > out->bwd_workspace_bytes) out->bwd_workspace_bytes = bwd;
   }
-  out->bwd_workspace_bytes = llsa::cross::bwd_work_bytes_simt(g, plan);
   return LLSA_OK;
 }
 
@@ -274,9 +274,9 @@ llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, cons
   LLSA_NEED(dv);
   LLSA_NEED(workspace);
   const llsa::cross::Keys keys{kv_len, key_mask};
-  if (llsa::cross::bwd_one_supported(g))
-    return llsa::launched(llsa::cross::launch_bwd_one(g, llsa::cross::plan_bwd_one(g, llsa::kSms), q, k, v, keys, d_o,
-                                                      lse, dq, dk, dv, workspace, (cudaStream_t)stream));
+  if (llsa::cross::bwd_tc_supported(g))
+    return llsa::launched(llsa::cross::launch_bwd_tc(g, llsa::kSms, q, k, v, keys, o, d_o, lse, dq, dk, dv, workspace,
+                                                     (cudaStream_t)stream));
   const llsa::cross::Plan plan = llsa::cross::plan_simt(g, llsa::kSms);
   return llsa::launched(llsa::cross::launch_bwd_simt(g, plan, q, k, v, keys, o, d_o, lse, dq, dk, dv, workspace,
                                                      (cudaStream_t)stream));
@@ -285,7 +285,7 @@ llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, cons
 llsa_status llsa_cross_attn_paths(const llsa_cross_problem* p, int* fwd_tc, int* bwd_tc) {
   LLSA_CROSS(p, g);
   if (fwd_tc) *fwd_tc = llsa::cross::fwd_tc_supported(g);
-  if (bwd_tc) *bwd_tc = llsa::cross::bwd_one_supported(g);
+  if (bwd_tc) *bwd_tc = llsa::cross::bwd_tc_supported(g);
   return LLSA_OK;
 }
 

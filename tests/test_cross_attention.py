@@ -194,9 +194,10 @@ def test_gradients_against_differences(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_same_bits_every_time_and_beyond_the_outputs_nothing_changes(dtype):
+@pytest.mark.parametrize("b,h,hk,nq,nk,d", [(2, 4, 2, 333, 517, 64), (2, 16, 16, 1100, 300, 72), (1, 4, 4, 5000, 77, 64),
+                                            (2, 8, 2, 1, 2000, 128), (1, 2, 1, 900, 1, 128)])
+def test_same_bits_every_time_and_beyond_the_outputs_nothing_changes(dtype, b, h, hk, nq, nk, d):
     gen = torch.Generator().manual_seed(6)
-    b, h, hk, nq, nk, d = 2, 4, 2, 333, 517, 64
     q, g = (util.tokens(gen, b, h, nq, d, dtype) for _ in range(2))
     k, v = (util.tokens(gen, b, hk, nk, d, dtype) for _ in range(2))
     p = llsa.CrossProblem(b, h, nq, nk, d, kv_heads=hk, dtype=NUMBER[dtype])
@@ -320,6 +321,19 @@ def problem(**kw):
 ])
 def test_validation(kw, status):
     assert llsa.cross_validate(problem(**kw)) == status
+
+
+def test_workspaces_hold_what_either_path_keeps():
+    """Whatever the strides, which decide between the paths: the row sums and every split's partial results."""
+    for kw in (dict(batch=4, heads=16, kv_heads=16, nq=4096, nk=300, d=72), dict(batch=1, heads=6, kv_heads=6, nq=65536),
+               dict(nq=1, nk=16384, d=128), dict(nq=64, nk=1000), dict(nq=4096, nk=4096)):
+        a, b = (llsa.cross_query_sizes(problem(dtype=t, **kw)) for t in (llsa.BF16, llsa.FP32))
+        assert a["fwd_workspace_bytes"] >= b["fwd_workspace_bytes"]
+        assert a["bwd_workspace_bytes"] >= b["bwd_workspace_bytes"], kw
+    s = llsa.cross_query_sizes(problem(batch=4, heads=16, kv_heads=16, nq=4096, nk=300, d=72))
+    rows, keys = 4 * 16 * 4096, 4 * 16 * 300
+    # 192 key tiles on 148 SMs: the queries are split, two partial gradients at least
+    assert s["bwd_workspace_bytes"] >= rows * 4 + 2 * 2 * keys * 72 * 4
 
 
 @pytest.mark.parametrize("name,strides,status", [
