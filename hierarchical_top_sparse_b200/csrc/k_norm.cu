@@ -4,12 +4,14 @@
 //   g = dy w,  xhat = (x - mean) rstd,
 //   dx = rstd (g - mean_c(g) - xhat mean_c(g xhat)),  dw = sum_rows dy xhat,  db = sum_rows dy.
 //
-// Bound by memory: every row is read once and kept in registers (the variance
-// is the mean of the squared deviations from the mean, in a second pass over
-// the registers, so that large offsets cost no digits).  G threads work on a
-// row, each on IT vectors of 16 bytes (single values where the width, a stride
-// or an address does not allow vectors); rows of up to 4 KB take a part of a warp or
-// a warp, wider ones a block.  Rows are walked in the order of x's memory.
+// Bound by memory: every row is read once and kept in registers as it came (the
+// variance is the mean of the squared deviations from the mean, in a second
+// pass over the registers, so that large offsets cost no digits).  G threads
+// work on a row, each on IT vectors of 16 bytes (single values where the width,
+// a stride or an address does not allow vectors); rows of up to 2 KB take a
+// part of a warp or a warp, wider ones a block.  R rows are taken at a time,
+// and the next R are on their way while these are worked on: an SM needs some
+// 40 KB in flight.  Rows are walked in the order of x's memory.
 //
 // In the backward every thread keeps the same channels for all its rows and
 // sums dy xhat and dy in registers; a block adds up its row groups (by
@@ -23,6 +25,7 @@ namespace norm {
 
 template <typename T, int V> struct Raw;
 template <> struct Raw<__nv_bfloat16, 8> { uint4 w; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 w; };
 template <> struct Raw<float, 4> { float4 w; };
 template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 w; };
 template <> struct Raw<float, 1> { float w; };
@@ -34,6 +37,12 @@ __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& r, float* f)
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 4>& r, float* f) {
+  f[0] = __uint_as_float(r.w.x << 16);
+  f[1] = __uint_as_float(r.w.x & 0xffff0000u);
+  f[2] = __uint_as_float(r.w.y << 16);
+  f[3] = __uint_as_float(r.w.y & 0xffff0000u);
 }
 __device__ __forceinline__ void unpack(const Raw<float, 4>& r, float* f) {
   f[0] = r.w.x;
@@ -50,6 +59,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ void pack(Raw<__nv_bfloat16, 8>& r, const float* f) {
   r.w = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+__device__ __forceinline__ void pack(Raw<__nv_bfloat16, 4>& r, const float* f) {
+  r.w = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
 }
 __device__ __forceinline__ void pack(Raw<float, 4>& r, const float* f) { r.w = make_float4(f[0], f[1], f[2], f[3]); }
 __device__ __forceinline__ void pack(Raw<__nv_bfloat16, 1>& r, const float* f) { r.w = __float2bfloat16_rn(f[0]); }
@@ -95,11 +107,59 @@ struct At {
 };
 __device__ __forceinline__ At place(const Geo& g, int64_t row) {
   const uint32_t r = (uint32_t)row;         // rows of a group are fewer than 2^31
-  const uint32_t q = r / g.n2;
-  return At{(int64_t)(q / g.n1), (int64_t)(q % g.n1), (int64_t)(r % g.n2)};
+  const uint32_t q = over(r, g.n2), p = over(q, g.n1);
+  return At{(int64_t)p, (int64_t)(q - p * g.n1.d), (int64_t)(r - q * g.n2.d)};
 }
 __device__ __forceinline__ int64_t offset(const At& a, const int64_t* st, int group) {
   return a.i0 * st[0] + a.i1 * st[1] + a.i2 * st[2] + group * st[3];
+}
+
+// Two fp32 values in one register pair, and the instructions that take both at
+// once: a norm's arithmetic per byte is enough to fill the issue slots.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 twice(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ float both(f2 v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// V values as pairs (of one value: its other half is zero).
+template <int V> constexpr int pairs() { return (V + 1) / 2; }
+template <typename T, int V>
+__device__ __forceinline__ void unpack2(const Raw<T, V>& r, f2* f) {
+  float x[V + 1];
+  unpack(r, x);
+  if (V == 1) x[1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < pairs<V>(); ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void pack2(Raw<T, V>& r, const f2* f) {
+  float x[V + 1];
+#pragma unroll
+  for (int i = 0; i < pairs<V>(); ++i) split(f[i], x[2 * i], x[2 * i + 1]);
+  pack(r, x);
 }
 
 // Sums N values over the G threads of a row.  Rows that span a block use
@@ -131,83 +191,142 @@ __device__ __forceinline__ void row_sum(float* v, float* red, int& turn) {
 
 template <int G> constexpr int threads() { return G <= 32 ? 256 : G; }
 
+// Rows of a step and thread group; two blocks of 256 threads, or one of 512, then have some 32 KB or more in flight.
+template <int G, int IT, int V> constexpr int rows_at_once() {
+  return G > 32 || V == 1 ? 1 : (IT == 1 ? 4 : (IT == 2 ? 2 : 1));
+}
+
 template <typename T, int V, int G, int IT>
 __global__ void __launch_bounds__(threads<G>()) fwd_kernel(const __grid_constant__ Geo g, const T* x, const void* w,
                                                            const void* b, T* y, float* mean, float* rstd) {
-  constexpr int RPB = threads<G>() / G;              // rows per block and step
+  constexpr int RPB = threads<G>() / G;              // thread groups of a block
+  constexpr int R = rows_at_once<G, IT, V>();
+  constexpr bool KEEP = G <= 32;                     // weights in registers; a block-wide row reads them again (from L1)
   __shared__ float red[G > 32 ? 2 * 32 : 1];
   int turn = 0;
   const int sub = threadIdx.x % G, slot = threadIdx.x / G;
   const int group = blockIdx.y;
   const float inv_c = 1.f / (float)g.c;
-  float wv[IT * V], bv[IT * V];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
+  constexpr int P = pairs<V>();
+  f2 wv[KEEP ? IT * P : 1], bv[KEEP ? IT * P : 1];
+  auto params = [&](int i, f2* ww, f2* bb) {
     const int c = (i * G + sub) * V;
+    float fw[V + 1], fb[V + 1];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      wv[i * V + e] = 1.f;
-      bv[i * V + e] = 0.f;
+    for (int e = 0; e < V + 1; ++e) {
+      fw[e] = 1.f;
+      fb[e] = 0.f;
     }
     if (c < g.c) {
-      if (w) load_param<V>(w, g.param_bf16, group * g.ws + c, wv + i * V);
-      if (b) load_param<V>(b, g.param_bf16, group * g.bs + c, bv + i * V);
+      if (w) load_param<V>(w, g.param_bf16, group * g.ws + c, fw);
+      if (b) load_param<V>(b, g.param_bf16, group * g.bs + c, fb);
     }
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      ww[e] = pair(fw[2 * e], fw[2 * e + 1]);
+      bb[e] = pair(fb[2 * e], fb[2 * e + 1]);
+    }
+  };
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) params(i, wv + i * P, bv + i * P);
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < g.rows; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t r = r0 + slot;
-    const bool live = r < g.rows;
-    const At at = place(g, live ? r : 0);
-    const T* px = x + offset(at, g.x, group);
-    Raw<T, V> raw[IT];
+  auto at_x = [&](int64_t r) { return g.flat_fwd ? r * g.x[2] + group * g.x[3] : offset(place(g, r), g.x, group); };
+  auto at_y = [&](int64_t r) { return g.flat_fwd ? r * g.y[2] + group * g.y[3] : offset(place(g, r), g.y, group); };
+  const int64_t step = (int64_t)gridDim.x * RPB * R;
+  Raw<T, V> next[R][IT];
+  auto fetch = [&](int64_t r0) {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (live && c < g.c) raw[i] = *reinterpret_cast<const Raw<T, V>*>(px + c);
-    }
-    float f[IT * V];
-    float sum[1] = {0.f};
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k * RPB + slot;
+      if (r >= g.rows) continue;
+      const T* px = x + at_x(r);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (live && c < g.c) {
-        unpack(raw[i], f + i * V);
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum[0] += f[i * V + e];
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * G + sub) * V;
+        if (c < g.c) next[k][i] = *reinterpret_cast<const Raw<T, V>*>(px + c);
       }
     }
-    row_sum<G, 1>(sum, red, turn);
-    const float mu = sum[0] * inv_c;
-    float sq[1] = {0.f};
+  };
+  fetch((int64_t)blockIdx.x * RPB * R);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB * R; r0 < g.rows; r0 += step) {
+    f2 f[R][IT * P];
+    float mu[R], rs[R];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (live && c < g.c)
+    for (int k = 0; k < R; ++k) {
+      f2 sum = twice(0.f);
+      const bool live = r0 + k * RPB + slot < g.rows;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          f[i * V + e] -= mu;
-          sq[0] = fmaf(f[i * V + e], f[i * V + e], sq[0]);
+      for (int i = 0; i < IT; ++i)
+        if (live && (i * G + sub) * V < g.c) {
+          unpack2(next[k][i], f[k] + i * P);
+#pragma unroll
+          for (int e = 0; e < P; ++e) sum = add2(sum, f[k][i * P + e]);
         }
+      mu[k] = both(sum);
     }
-    row_sum<G, 1>(sq, red, turn);
-    const float rs = 1.f / sqrtf(fmaf(sq[0], inv_c, g.eps));
-    if (!live) continue;
-    T* py = y + offset(at, g.y, group);
+    fetch(r0 + step);
+    row_sum<G, R>(mu, red, turn);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (c >= g.c) continue;
-      float out[V];
+    for (int k = 0; k < R; ++k) {
+      mu[k] *= inv_c;
+      const f2 minus = V == 1 ? pair(-mu[k], 0.f) : twice(-mu[k]);
+      f2 sum = twice(0.f);
+      const bool live = r0 + k * RPB + slot < g.rows;
 #pragma unroll
-      for (int e = 0; e < V; ++e) out[e] = fmaf(f[i * V + e] * rs, wv[i * V + e], bv[i * V + e]);
-      Raw<T, V> o;
-      pack(o, out);
-      *reinterpret_cast<Raw<T, V>*>(py + c) = o;
+      for (int i = 0; i < IT; ++i)
+        if (live && (i * G + sub) * V < g.c) {
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            f[k][i * P + e] = add2(f[k][i * P + e], minus);
+            sum = fma2(f[k][i * P + e], f[k][i * P + e], sum);
+          }
+        }
+      rs[k] = both(sum);
     }
-    if (sub == 0) {
-      const int64_t st = offset(at, g.s, group);
-      if (mean) mean[st] = mu;
-      if (rstd) rstd[st] = rs;
+    row_sum<G, R>(rs, red, turn);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k * RPB + slot;
+      rs[k] = rsqrtf(fmaf(rs[k], inv_c, g.eps));
+      if (r >= g.rows) continue;
+      const f2 rk = twice(rs[k]);
+      T* py = y + at_y(r);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * G + sub) * V;
+        if (c >= g.c) continue;
+        f2 ww[P], bb[P];
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            ww[e] = wv[i * P + e];
+            bb[e] = bv[i * P + e];
+          }
+        } else {
+          params(i, ww, bb);
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) f[k][i * P + e] = fma2(mul2(f[k][i * P + e], rk), ww[e], bb[e]);
+        Raw<T, V> o;
+        pack2(o, f[k] + i * P);
+        *reinterpret_cast<Raw<T, V>*>(py + c) = o;
+      }
+    }
+    if (mean || rstd) {                              // thread k of a row's threads: the k-th row's statistics
+      float m = mu[0], v = rs[0];
+#pragma unroll
+      for (int k = 1; k < R; ++k)
+        if (sub == k) {
+          m = mu[k];
+          v = rs[k];
+        }
+      const int64_t r = r0 + sub * RPB + slot;
+      if (sub < R && r < g.rows) {
+        const int64_t st = offset(place(g, r), g.s, group);
+        if (mean) mean[st] = m;
+        if (rstd) rstd[st] = v;
+      }
     }
   }
 }
@@ -218,6 +337,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
                                                            const float* __restrict__ rstd, T* dx,
                                                            float* __restrict__ part) {
   constexpr int RPB = threads<G>() / G;
+  constexpr int R = G > 32 || V == 1 || IT > 1 ? 1 : 2;
   constexpr int NV = IT * V;
   __shared__ float red[G > 32 ? 2 * 2 * 32 : 1];
   __shared__ float cols[G <= 32 ? 8 * G * NV : 1];   // a block's eight warps' sums
@@ -225,89 +345,122 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
   const int sub = threadIdx.x % G, slot = threadIdx.x / G;
   const int group = blockIdx.y;
   const float inv_c = 1.f / (float)g.c;
-  // narrow rows keep the weights in registers; a block-wide row reads them again (from L1)
-  float wv[G <= 32 ? NV : 1];
-  if constexpr (G <= 32) {
+  constexpr int P = pairs<V>();
+  constexpr bool KEEP = G <= 32;
+  f2 wv[KEEP ? IT * P : 1];
+  auto weights = [&](int i, f2* ww) {
+    const int c = (i * G + sub) * V;
+    float fw[V + 1];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
+    for (int e = 0; e < V + 1; ++e) fw[e] = 1.f;
+    if (w && c < g.c) load_param<V>(w, g.param_bf16, group * g.ws + c, fw);
 #pragma unroll
-      for (int e = 0; e < V; ++e) wv[i * V + e] = 1.f;
-      if (w && c < g.c) load_param<V>(w, g.param_bf16, group * g.ws + c, wv + i * V);
-    }
+    for (int e = 0; e < P; ++e) ww[e] = pair(fw[2 * e], fw[2 * e + 1]);
+  };
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) weights(i, wv + i * P);
   }
-  float dw[NV], db[NV];
+  auto weights_of = [&](int i, f2* ww) {
+    if constexpr (KEEP) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) dw[i] = db[i] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < g.rows; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t r = r0 + slot;
-    const bool live = r < g.rows;
-    const At at = place(g, live ? r : 0);
-    const T* px = x + offset(at, g.x, group);
-    const T* pg = dy + offset(at, g.dy, group);
-    const int64_t st = offset(at, g.s, group);
-    Raw<T, V> rx[IT], rg[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (live && c < g.c) {
-        rx[i] = *reinterpret_cast<const Raw<T, V>*>(px + c);
-        rg[i] = *reinterpret_cast<const Raw<T, V>*>(pg + c);
-      }
+      for (int e = 0; e < P; ++e) ww[e] = wv[i * P + e];
+    } else {
+      weights(i, ww);
     }
-    const float mu = live ? mean[st] : 0.f, rs = live ? rstd[st] : 0.f;
-    float sum[2] = {0.f, 0.f};
+  };
+  f2 dw[IT * P], db[IT * P];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * G + sub) * V;
-      if (live && c < g.c) {
-        float fx[V], fg[V], ww[V];
-        unpack(rx[i], fx);
-        unpack(rg[i], fg);
-        if constexpr (G <= 32) {
+  for (int i = 0; i < IT * P; ++i) dw[i] = db[i] = twice(0.f);
+  const int64_t step = (int64_t)gridDim.x * RPB * R;
+  Raw<T, V> nx[R][IT], ng[R][IT];
+  float nmu[R], nrs[R];
+  auto fetch = [&](int64_t r0) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) ww[e] = wv[i * V + e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) ww[e] = 1.f;
-          if (w) load_param<V>(w, g.param_bf16, group * g.ws + c, ww);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (fx[e] - mu) * rs, gw = fg[e] * ww[e];
-          sum[0] += gw;
-          sum[1] = fmaf(gw, xh, sum[1]);
-          dw[i * V + e] = fmaf(fg[e], xh, dw[i * V + e]);
-          db[i * V + e] += fg[e];
-        }
-      }
-    }
-    if (dx) {                                          // uniform over the grid
-      row_sum<G, 2>(sum, red, turn);
-      const float c1 = sum[0] * inv_c, c2 = sum[1] * inv_c;
-      T* po = dx + offset(at, g.dx, group);
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k * RPB + slot;
+      if (r >= g.rows) continue;
+      const At at = place(g, r);
+      const T* px = x + (g.flat_bwd ? r * g.x[2] + group * g.x[3] : offset(at, g.x, group));
+      const T* pg = dy + (g.flat_bwd ? r * g.dy[2] + group * g.dy[3] : offset(at, g.dy, group));
+      const int64_t st = offset(at, g.s, group);
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         const int c = (i * G + sub) * V;
-        if (live && c < g.c) {
-          float fx[V], fg[V], ww[V];
-          unpack(rx[i], fx);
-          unpack(rg[i], fg);
-          if constexpr (G <= 32) {
+        if (c < g.c) {
+          nx[k][i] = *reinterpret_cast<const Raw<T, V>*>(px + c);
+          ng[k][i] = *reinterpret_cast<const Raw<T, V>*>(pg + c);
+        }
+      }
+      nmu[k] = mean[st];
+      nrs[k] = rstd[st];
+    }
+  };
+  fetch((int64_t)blockIdx.x * RPB * R);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB * R; r0 < g.rows; r0 += step) {
+    Raw<T, V> rx[R][IT], rg[R][IT];
+    float mu[R], rs[R];
 #pragma unroll
-            for (int e = 0; e < V; ++e) ww[e] = wv[i * V + e];
-          } else {
+    for (int k = 0; k < R; ++k) {
+      mu[k] = nmu[k];
+      rs[k] = nrs[k];
 #pragma unroll
-            for (int e = 0; e < V; ++e) ww[e] = 1.f;
-            if (w) load_param<V>(w, g.param_bf16, group * g.ws + c, ww);
+      for (int i = 0; i < IT; ++i) {
+        rx[k][i] = nx[k][i];
+        rg[k][i] = ng[k][i];
+      }
+    }
+    fetch(r0 + step);
+    float sum[2 * R];
+    f2 shift[R], scale[R];                             // xhat = x rstd - mean rstd
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      scale[k] = twice(rs[k]);
+      shift[k] = twice(-mu[k] * rs[k]);
+      f2 s0 = twice(0.f), s1 = twice(0.f);
+      const bool live = r0 + k * RPB + slot < g.rows;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+        if (live && (i * G + sub) * V < g.c) {
+          f2 fx[P], fg[P], ww[P];
+          unpack2(rx[k][i], fx);
+          unpack2(rg[k][i], fg);
+          weights_of(i, ww);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2 xh = fma2(fx[e], scale[k], shift[k]), gw = mul2(fg[e], ww[e]);
+            s0 = add2(s0, gw);
+            s1 = fma2(gw, xh, s1);
+            dw[i * P + e] = fma2(fg[e], xh, dw[i * P + e]);
+            db[i * P + e] = add2(db[i * P + e], fg[e]);
           }
+        }
+      sum[2 * k] = both(s0);                           // (the empty half of a single value has dy = 0)
+      sum[2 * k + 1] = both(s1);
+    }
+    if (dx) {                                          // uniform over the grid
+      row_sum<G, 2 * R>(sum, red, turn);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float xh = (fx[e] - mu) * rs, gw = fg[e] * ww[e];
-            fx[e] = rs * (gw - c1 - xh * c2);
+      for (int k = 0; k < R; ++k) {
+        const int64_t r = r0 + k * RPB + slot;
+        if (r >= g.rows) continue;
+        const f2 c1 = twice(-sum[2 * k] * inv_c * rs[k]), c2 = twice(-sum[2 * k + 1] * inv_c);
+        T* po = dx + (g.flat_bwd ? r * g.dx[2] + group * g.dx[3] : offset(place(g, r), g.dx, group));
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int c = (i * G + sub) * V;
+          if (c >= g.c) continue;
+          f2 fx[P], fg[P], ww[P];
+          unpack2(rx[k][i], fx);
+          unpack2(rg[k][i], fg);
+          weights_of(i, ww);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2 xh = fma2(fx[e], scale[k], shift[k]);
+            fx[e] = fma2(fma2(xh, c2, mul2(fg[e], ww[e])), scale[k], c1);   // rstd (g - xhat c2) - rstd c1
           }
           Raw<T, V> o;
-          pack(o, fx);
+          pack2(o, fx);
           *reinterpret_cast<Raw<T, V>*>(po + c) = o;
         }
       }
@@ -315,6 +468,12 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
   }
   if (!part) return;
   float* out = part + ((int64_t)group * gridDim.x + blockIdx.x) * 2 * g.c;
+  float sw[IT * P * 2], sb[IT * P * 2];                // value e of vector i at 2 P i + e
+#pragma unroll
+  for (int i = 0; i < IT * P; ++i) {
+    split(dw[i], sw[2 * i], sw[2 * i + 1]);
+    split(db[i], sb[2 * i], sb[2 * i + 1]);
+  }
   if constexpr (G > 32) {
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -322,18 +481,18 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
       if (c < g.c)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          out[c + e] = dw[i * V + e];
-          out[g.c + c + e] = db[i * V + e];
+          out[c + e] = sw[2 * P * i + e];
+          out[g.c + c + e] = sb[2 * P * i + e];
         }
     }
   } else {
     // the row groups of a warp by shuffles, then the eight warps in order
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < IT * P * 2; ++i)
 #pragma unroll
       for (int s = 16; s >= G; s >>= 1) {
-        dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], s);
-        db[i] += __shfl_xor_sync(0xffffffffu, db[i], s);
+        sw[i] += __shfl_xor_sync(0xffffffffu, sw[i], s);
+        sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], s);
       }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -341,7 +500,10 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
       __syncthreads();
       if (lane < G)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) cols[(warp * NV + i) * G + lane] = which ? db[i] : dw[i];
+        for (int i = 0; i < NV; ++i) {
+          const int at = (i / V) * 2 * P + i % V;
+          cols[(warp * NV + i) * G + lane] = which ? sb[at] : sw[at];
+        }
       __syncthreads();
       for (int j = threadIdx.x; j < G * NV; j += 256) {
         float x = 0.f;
@@ -366,7 +528,7 @@ __global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ 
   const float* p = part + (int64_t)group * parts * 2 * c + which * c;
   float x = 0.f;
   if (col < c)
-#pragma unroll 4
+#pragma unroll 8
     for (int k = y; k < parts; k += 32) x += p[(int64_t)k * 2 * c + col];
   s[y][lane] = x;
   __syncthreads();
@@ -385,93 +547,109 @@ __global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ 
 
 // ------------------------------------------------------------------ host
 
-// Threads per row and vectors per thread.  Vectors: the narrowest set of
-// threads whose registers hold the row with at most 4 vectors each; single
-// values: up to 16 of them.
+// Values per load, threads per row and loads per thread.  A row's threads are
+// the fewest that hold it in a few registers: in the backward, which keeps two
+// sums for each channel of a thread, about 16 channels each, in the forward up
+// to 32.  257 to 384 bf16 channels take 8-byte loads, which fill a warp where
+// 16-byte ones would leave a quarter of it (or, with 16 threads a row, need the
+// registers of 24 channels: 150, and one block an SM).
 struct Shape {
-  int g, it;
+  int v, g, it;
 };
-static Shape shape_of(const Geo& g) {
+static Shape shape_of(const Geo& g, bool bwd) {
   if (g.vec) {
-    const int n = g.c / (g.bf16 ? 8 : 4);
-    if (n <= 8) return {8, 1};
-    if (n <= 16) return {16, 1};
-    if (n <= 32) return {32, 1};
-    if (n <= 48) return {16, 3};
-    if (n <= 64) return {32, 2};
-    if (n <= 96) return {32, 3};
-    if (n <= 128) return {32, 4};
-    if (n <= 256) return {128, 2};
-    if (n <= 512) return {256, 2};
-    if (n <= 1024) return {512, 2};
-    if (n <= 2048) return {512, 4};
-    return {1024, 4};
+    const int v = g.bf16 ? 8 : 4, n = g.c / v;
+    if (n <= 8) return {v, 8, 1};
+    if (n <= 16) return {v, 16, 1};
+    if (n <= 32) return {v, 32, 1};
+    if (n <= 48) return g.bf16 ? Shape{4, 32, 3} : Shape{4, 16, 3};
+    if (n <= 64) return {v, 32, 2};
+    if (bwd) {
+      if (n <= 128) return {v, 128, 1};
+      if (n <= 256) return {v, 256, 1};
+      if (n <= 512) return {v, 512, 1};
+    } else {
+      if (n <= 96) return {v, 32, 3};
+      if (n <= 128) return {v, 32, 4};
+      if (n <= 256) return {v, 128, 2};
+      if (n <= 512) return {v, 256, 2};
+    }
+    if (n <= 1024) return {v, 512, 2};
+    if (n <= 2048) return {v, 512, 4};
+    return {v, 1024, 4};
   }
-  if (g.c <= 8) return {8, 1};
-  if (g.c <= 32) return {32, 1};
-  if (g.c <= 128) return {32, 4};
-  if (g.c <= 256) return {32, 8};
-  if (g.c <= 1024) return {128, 8};
-  if (g.c <= 4096) return {512, 8};
-  return {1024, 16};
+  if (g.c <= 8) return {1, 8, 1};
+  if (g.c <= 32) return {1, 32, 1};
+  if (g.c <= 128) return {1, 32, 4};
+  if (g.c <= 256) return {1, 32, 8};
+  if (g.c <= 1024) return bwd ? Shape{1, 256, 4} : Shape{1, 128, 8};
+  if (g.c <= 4096) return {1, 512, 8};
+  return {1, 1024, 16};
 }
 
 static int rows_per_block(const Shape& s) { return s.g <= 32 ? 256 / s.g : 1; }
 
 // Blocks per group in the backward: enough to fill the device, no more than there are row steps.
 int bwd_parts(const Geo& g) {
-  const Shape s = shape_of(g);
-  const int64_t steps = (g.rows + rows_per_block(s) - 1) / rows_per_block(s);
-  const int per_sm = s.g <= 32 ? 4 : (s.g <= 256 ? 4 : (s.g <= 512 ? 2 : 1));
+  const Shape s = shape_of(g, true);
+  const int rows = rows_per_block(s);
+  const int64_t steps = (g.rows + rows - 1) / rows;
+  const int per_sm = s.g <= 32 ? 2 : (s.g <= 256 ? 4 : (s.g <= 512 ? 2 : 1));
   const int64_t want = (kSms * per_sm + g.groups - 1) / g.groups;
   return (int)(steps < want ? steps : want);
 }
 
-#define NORM_VEC_SHAPES(F, T, V) \
-  F(T, V, 8, 1) F(T, V, 16, 1) F(T, V, 32, 1) F(T, V, 16, 3) F(T, V, 32, 2) F(T, V, 32, 3) F(T, V, 32, 4) \
-  F(T, V, 128, 2) F(T, V, 256, 2) F(T, V, 512, 2) F(T, V, 512, 4)
+#define NORM_BOTH_SHAPES(F, T, V) \
+  F(T, V, 8, 1) F(T, V, 16, 1) F(T, V, 32, 1) F(T, V, 32, 2) F(T, V, 512, 2) F(T, V, 512, 4)
+#define NORM_FWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 32, 3) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 256, 2)
+#define NORM_BWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 128, 1) F(T, V, 256, 1) F(T, V, 512, 1)
 #define NORM_ONE_SHAPES(F, T) \
-  F(T, 1, 8, 1) F(T, 1, 32, 1) F(T, 1, 32, 4) F(T, 1, 32, 8) F(T, 1, 128, 8) F(T, 1, 512, 8) F(T, 1, 1024, 16)
+  F(T, 1, 8, 1) F(T, 1, 32, 1) F(T, 1, 32, 4) F(T, 1, 32, 8) F(T, 1, 512, 8) F(T, 1, 1024, 16)
 
 cudaError_t launch_fwd(const Geo& g, const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                        cudaStream_t s) {
-  const Shape sh = shape_of(g);
-  const int64_t steps = (g.rows + rows_per_block(sh) - 1) / rows_per_block(sh);
+  const Shape sh = shape_of(g, false);
+  const int rows = rows_per_block(sh);
+  const int64_t steps = (g.rows + rows - 1) / rows;
   const int64_t most = (int64_t)kSms * (sh.g <= 256 ? 8 : (sh.g <= 512 ? 4 : 2));
   const int64_t want = (most + g.groups - 1) / g.groups;
   const dim3 grid((unsigned)(steps < want ? steps : want), (unsigned)g.groups);
 #define NORM_FWD(T, VV, GG, II)                                                                              \
-  if (sh.g == GG && sh.it == II) {                                                                           \
+  if (sh.v == VV && sh.g == GG && sh.it == II) {                                                                           \
     fwd_kernel<T, VV, GG, II><<<grid, threads<GG>(), 0, s>>>(g, (const T*)x, w, b, (T*)y, mean, rstd);       \
     note_launches(1);                                                                                        \
     return cudaGetLastError();                                                                               \
   }
   if (g.bf16) {
-    if (g.vec) { NORM_VEC_SHAPES(NORM_FWD, __nv_bfloat16, 8) } else { NORM_ONE_SHAPES(NORM_FWD, __nv_bfloat16) }
+    NORM_FWD_SHAPES(NORM_FWD, __nv_bfloat16, 8) NORM_FWD(__nv_bfloat16, 4, 32, 3)
+    NORM_ONE_SHAPES(NORM_FWD, __nv_bfloat16) NORM_FWD(__nv_bfloat16, 1, 128, 8)
   } else {
-    if (g.vec) { NORM_VEC_SHAPES(NORM_FWD, float, 4) NORM_FWD(float, 4, 1024, 4) } else { NORM_ONE_SHAPES(NORM_FWD, float) }
+    NORM_FWD_SHAPES(NORM_FWD, float, 4) NORM_FWD(float, 4, 16, 3) NORM_FWD(float, 4, 1024, 4)
+    NORM_ONE_SHAPES(NORM_FWD, float) NORM_FWD(float, 1, 128, 8)
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_bwd(const Geo& g, const void* x, const void* dy, const void* w, const float* mean,
                        const float* rstd, void* dx, void* dw, void* db, void* work, cudaStream_t s) {
-  const Shape sh = shape_of(g);
+  const Shape sh = shape_of(g, true);
   const int parts = bwd_parts(g);
   const dim3 grid((unsigned)parts, (unsigned)g.groups);
   float* part = (dw || db) ? static_cast<float*>(work) : nullptr;
   cudaError_t e = cudaErrorInvalidValue;
 #define NORM_BWD(T, VV, GG, II)                                                                                     \
-  if (sh.g == GG && sh.it == II) {                                                                                  \
+  if (sh.v == VV && sh.g == GG && sh.it == II) {                                                                                  \
     bwd_kernel<T, VV, GG, II>                                                                                       \
         <<<grid, threads<GG>(), 0, s>>>(g, (const T*)x, (const T*)dy, w, mean, rstd, (T*)dx, part);                 \
     note_launches(1);                                                                                               \
     e = cudaGetLastError();                                                                                         \
   }
   if (g.bf16) {
-    if (g.vec) { NORM_VEC_SHAPES(NORM_BWD, __nv_bfloat16, 8) } else { NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) }
+    NORM_BWD_SHAPES(NORM_BWD, __nv_bfloat16, 8) NORM_BWD(__nv_bfloat16, 4, 32, 3)
+    NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4)
   } else {
-    if (g.vec) { NORM_VEC_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 1024, 4) } else { NORM_ONE_SHAPES(NORM_BWD, float) }
+    NORM_BWD_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 16, 3) NORM_BWD(float, 4, 1024, 4)
+    NORM_ONE_SHAPES(NORM_BWD, float) NORM_BWD(float, 1, 256, 4)
   }
   if (e != cudaSuccess || !part) return e;
   const dim3 fgrid((unsigned)((g.c + 31) / 32), (unsigned)g.groups, 2);

@@ -102,9 +102,7 @@ static llsa_status make_cross(const llsa_cross_problem* p, cross::Geo* g) {
   return LLSA_OK;
 }
 
-// Rows as nested loops in the order of x's memory; two neighbouring loops are
-// joined where the outer one's stride is the inner one's stride times its
-// count in every tensor that is walked.
+// Rows as nested loops in the order of x's memory.
 static llsa_status make_norm(const llsa_norm_problem* p, norm::Geo* g) {
   if (!p) return LLSA_ERR_ARG;
   memset(g, 0, sizeof(*g));
@@ -152,28 +150,20 @@ static llsa_status make_norm(const llsa_norm_problem* p, norm::Geo* g) {
         order[i] = order[j];
         order[j] = t;
       }
-  int64_t ln[3], ls[5][3];
-  int loops = 0;
-  for (int i = count - 1; i >= 0; --i) {        // innermost first, joining neighbours that run on
-    const int dim = order[i];
-    bool joins = loops > 0;
-    for (int t = 0; t < 5 && joins; ++t) joins = st[t][dim] == ls[t][loops - 1] * ln[loops - 1];
-    if (joins) {
-      ln[loops - 1] *= size[dim];
-    } else {
-      ln[loops] = size[dim];
-      for (int t = 0; t < 5; ++t) ls[t][loops] = st[t][dim];
-      ++loops;
-    }
+  int64_t ln[3] = {1, 1, 1}, ls[5][3] = {};     // innermost first
+  bool flat[4] = {true, true, true, true};
+  for (int i = 0; i < count; ++i) {
+    const int dim = order[count - 1 - i];
+    ln[i] = size[dim];
+    for (int t = 0; t < 5; ++t) ls[t][i] = st[t][dim];
+    for (int t = 0; t < 4; ++t) flat[t] = flat[t] && (i == 0 || ls[t][i] == ls[t][i - 1] * ln[i - 1]);
   }
-  for (; loops < 3; ++loops) {
-    ln[loops] = 1;
-    for (int t = 0; t < 5; ++t) ls[t][loops] = 0;
-  }
+  g->flat_fwd = flat[0] && flat[1];
+  g->flat_bwd = flat[0] && flat[2] && flat[3];
   g->groups = p->per_batch ? p->batch : 1;
   g->rows = ln[0] * ln[1] * ln[2];
-  g->n2 = (uint32_t)ln[0];
-  g->n1 = (uint32_t)ln[1];
+  g->n2 = norm::divisor((uint32_t)ln[0]);
+  g->n1 = norm::divisor((uint32_t)ln[1]);
   for (int t = 0; t < 5; ++t) {
     for (int i = 0; i < 3; ++i) out[t][2 - i] = ls[t][i];
     out[t][3] = st[t][0];

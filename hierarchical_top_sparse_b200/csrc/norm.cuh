@@ -6,15 +6,32 @@
 namespace llsa {
 namespace norm {
 
+// Division of 32-bit numbers by a fixed one, as a product (Granlund and
+// Montgomery, Division by Invariant Integers using Multiplication, 1994).
+struct Divisor {
+  uint32_t d, m, s;
+};
+inline Divisor divisor(uint32_t d) {
+  int l = 0;
+  while (l < 32 && (1ull << l) < d) ++l;
+  return Divisor{d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), (uint32_t)l};
+}
+__host__ __device__ inline uint32_t over(uint32_t n, const Divisor& v) {
+  const uint32_t t = (uint32_t)(((uint64_t)v.m * n) >> 32);
+  return v.s == 0 ? n : (t + ((n - t) >> 1)) >> (v.s - 1);
+}
+
 // Rows in the order of x's memory: three nested runs, the innermost last, with
-// the element strides of every tensor (s: of mean / rstd) in each run.  Rows
-// are dealt out in groups that share weight and bias (one group, or one per
-// batch row).
+// the element strides of every tensor (s: of mean / rstd) in each run; where
+// the rows of all tensors of a call lie a fixed stride apart it is flat, and
+// row r is at r times that stride.  Rows are dealt out in groups that share
+// weight and bias (one group, or one per batch row).
 struct Geo {
   int groups;
   int64_t rows;              // per group
-  uint32_t n1, n2;           // rows = n0 * n1 * n2 (n0 implied)
+  Divisor n1, n2;            // rows = n0 * n1 * n2 (n0 implied)
   int64_t x[4], y[4], dy[4], dx[4], s[4];   // [0..2]: runs, outermost first; [3]: group
+  int flat_fwd, flat_bwd;    // flat: the stride is that of the innermost run
   int64_t ws, bs;            // between the groups' weights and biases
   int c;
   float eps;

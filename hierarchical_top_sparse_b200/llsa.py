@@ -34,7 +34,9 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import lru_cache
 from math import sqrt
+from struct import Struct
 from typing import Optional
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libllsa.so")
@@ -130,13 +132,13 @@ def lib() -> ctypes.CDLL:
             "llsa_attn_paths": ([P, ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
             "llsa_cross_validate": ([X], i32),
             "llsa_cross_query_sizes": ([X, ctypes.POINTER(CCrossBuffers)], i32),
-            "llsa_cross_attn_fwd": ([X] + [vp] * 9, i32),
-            "llsa_cross_attn_bwd": ([X] + [vp] * 13, i32),
+            "llsa_cross_attn_fwd": ([vp] * 10, i32),
+            "llsa_cross_attn_bwd": ([vp] * 14, i32),
             "llsa_cross_attn_paths": ([X, ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
             "llsa_norm_validate": ([M], i32),
             "llsa_norm_query_sizes": ([M, ctypes.POINTER(CNormBuffers)], i32),
-            "llsa_layer_norm_fwd": ([M] + [vp] * 7, i32),
-            "llsa_layer_norm_bwd": ([M] + [vp] * 10, i32),
+            "llsa_layer_norm_fwd": ([vp] * 8, i32),
+            "llsa_layer_norm_bwd": ([vp] * 11, i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -373,26 +375,40 @@ class Pipeline:
 
 
 # ------------------------------------------------------------------ cross attention and layer norm
+#
+# A call's time on the host is that of a small kernel: the C problem is packed from its fixed part, made once for
+# each set of fields, and the tensors' strides.
 
-def _checked(name: str, x, shape, dtype: int, device):
-    """x as this call takes it: a CUDA tensor of this shape and type whose last dimension is contiguous."""
-    if tuple(x.shape) != shape:
+_NO_STRIDES = (0, 0, 0)
+
+
+def _checked(name: str, x, shape, dt, device):
+    """The address of x, a CUDA tensor of this shape and type whose last dimension is contiguous."""
+    if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
-    if x.dtype != _torch_dtype(dtype):
-        raise ValueError(f"{name}: {x.dtype}, expected {_torch_dtype(dtype)}")
+    if x.dtype != dt:
+        raise ValueError(f"{name}: {x.dtype}, expected {dt}")
     if x.device != device:
         raise ValueError(f"{name}: on {x.device}, expected {device}")
-    if shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension is not contiguous")
     return x.data_ptr()
 
 
-def _flat(name: str, x, shape, dtype, device):
-    """A contiguous tensor of this shape (or an int address, or None)."""
+def _strides(name: str, x):
+    """Batch, head and token stride."""
+    s = x.stride()
+    if s[3] != 1 and x.shape[3] > 1:
+        raise ValueError(f"{name}: the last dimension is not contiguous")
+    if s[0] == s[1] == s[2] == 0 and x.shape[:3].numel() > 1:      # zeros stand for the contiguous layout
+        raise ValueError(f"{name}: one token expanded over every dimension; materialise at least one of them")
+    return s[:3]
+
+
+def _flat(name: str, x, shape, dt, device):
+    """The address of a contiguous tensor of this shape (or an int address, or None)."""
     if x is None or isinstance(x, int):
         return x
-    if tuple(x.shape) != shape or x.dtype != dtype or x.device != device or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
+    if x.shape != shape or x.dtype != dt or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dt} tensor of shape {shape} on {device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
@@ -410,38 +426,26 @@ def _torch_dtype(dtype: int):
     return torch.bfloat16 if dtype == BF16 else torch.float32
 
 
-def _strided(name: str, cs: CStrides, x):
-    s = x.stride()
-    if s[0] == s[1] == s[2] == 0 and x.shape[:3].numel() > 1:      # zeros stand for the contiguous layout
-        raise ValueError(f"{name}: one token expanded over every dimension; materialise at least one of them")
-    cs.batch, cs.head, cs.token = s[0], s[1], s[2]
-
-
-class _On:
-    """The tensors' device as the current one, and the stream of a call: the given one, else the device's current one."""
-
-    __slots__ = ("index", "before", "stream")
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"tensors on {device}: these calls take CUDA tensors")
-        self.index = device.index
-        self.before = torch.cuda.current_device()
-        if stream is None:
-            stream = torch.cuda.current_stream(self.index)
-        self.stream = stream if isinstance(stream, int) else stream.cuda_stream
-
-    def __enter__(self):
-        if self.before != self.index:
-            import torch
-            torch.cuda.set_device(self.index)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            import torch
-            torch.cuda.set_device(self.before)
+def _run(fn, what: str, device, stream, *args):
+    """The call on the tensors' device, and on the given stream, else on the device's current one."""
+    from torch import cuda
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}: these calls take CUDA tensors")
+    if stream is None:
+        stream = cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    before = cuda.current_device()
+    if before == device.index:
+        st = fn(*args, stream)
+    else:
+        cuda.set_device(device)
+        try:
+            st = fn(*args, stream)
+        finally:
+            cuda.set_device(before)
+    if st != 0:
+        raise LLSAError(st, what)
 
 
 @dataclass
@@ -493,21 +497,33 @@ def cross_attn_paths(p: CrossProblem) -> dict:
     return {"fwd": name[f.value], "bwd": name[b.value]}
 
 
-def _cross_args(p: CrossProblem, named, kv_len, key_mask):
-    """The C problem with the tensors' strides, their addresses, and the addresses of kv_len and key_mask."""
+_PACK_CROSS = Struct("24q").pack          # q, k, v, o, d_o, dq, dk, dv
+_PACK_NORM = Struct("14q").pack           # x, y, dy, dx, weight_batch, bias_batch
+_CROSS_HEAD = CCrossProblem.q.offset
+_NORM_HEAD = CNormProblem.x.offset
+
+
+@lru_cache(maxsize=256)
+def _cross_fixed(batch, heads, kv_heads, nq, nk, d, scale, dtype):
+    """The C problem up to its strides, buffer sizes, shapes of q and k, element type."""
+    p = CrossProblem(batch, heads, nq, nk, d, kv_heads, scale, dtype)
+    sizes = cross_query_sizes(p)
+    return bytes(p.c())[:_CROSS_HEAD], sizes, p.q_shape, p.k_shape, _torch_dtype(dtype)
+
+
+def _cross_of(p: CrossProblem):
+    return _cross_fixed(p.batch, p.heads, p.kv_heads, p.nq, p.nk, p.d, p.scale, p.dtype)
+
+
+def _key_args(p: CrossProblem, kv_len, key_mask, device):
     import torch
-    c = p.c()
-    device = named[0][1].device
-    qs, ks = p.q_shape, p.k_shape
-    ptrs = []
-    for name, x in named:
-        ptrs.append(_checked(name, x, ks if name in ("k", "v", "dk", "dv") else qs, p.dtype, device))
-        _strided(name, getattr(c, "d_o" if name == "dO" else name), x)
-    n = _flat("kv_len", kv_len, (p.batch,), torch.int32, device)
-    m = key_mask
-    if m is not None and not isinstance(m, int) and m.dtype == torch.bool:
-        m = m.view(torch.uint8)
-    return c, device, ptrs, n, _flat("key_mask", m, (p.batch, p.nk), torch.uint8, device)
+    if kv_len is not None:
+        kv_len = _flat("kv_len", kv_len, (p.batch,), torch.int32, device)
+    if key_mask is not None and not isinstance(key_mask, int):
+        if key_mask.dtype == torch.bool:
+            key_mask = key_mask.view(torch.uint8)
+        key_mask = _flat("key_mask", key_mask, (p.batch, p.nk), torch.uint8, device)
+    return kv_len, key_mask
 
 
 def cross_attn_fwd(p: CrossProblem, q, k, v, o, lse=None, kv_len=None, key_mask=None, workspace=None, stream=None):
@@ -515,25 +531,33 @@ def cross_attn_fwd(p: CrossProblem, q, k, v, o, lse=None, kv_len=None, key_mask=
     int32 [batch] or None; key_mask: bool or uint8 [batch, nk], nonzero where the key is attended to, or None;
     workspace: fwd_workspace_bytes of device memory."""
     import torch
-    c, device, a, n, m = _cross_args(p, (("q", q), ("k", k), ("v", v), ("o", o)), kv_len, key_mask)
-    ls = _flat("lse", lse, p.q_shape[:3], torch.float32, device)
-    need = cross_query_sizes(p)["fwd_workspace_bytes"]
-    with _On(device, stream) as s:
-        _check(lib().llsa_cross_attn_fwd(ctypes.byref(c), a[0], a[1], a[2], n, m, a[3], ls,
-                                         _work(workspace, need, device), s), "cross_attn_fwd")
+    fixed, sizes, qs, ks, dt = _cross_of(p)
+    device = q.device
+    a = (_checked("q", q, qs, dt, device), _checked("k", k, ks, dt, device), _checked("v", v, ks, dt, device))
+    ao = _checked("o", o, qs, dt, device)
+    c = fixed + _PACK_CROSS(*_strides("q", q), *_strides("k", k), *_strides("v", v), *_strides("o", o),
+                            *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES)
+    n, m = _key_args(p, kv_len, key_mask, device)
+    ls = _flat("lse", lse, qs[:3], torch.float32, device)
+    _run(lib().llsa_cross_attn_fwd, "cross_attn_fwd", device, stream, c, *a, n, m, ao, ls,
+         _work(workspace, sizes["fwd_workspace_bytes"], device))
 
 
 def cross_attn_bwd(p: CrossProblem, q, k, v, o, dO, lse, dq, dk, dv, kv_len=None, key_mask=None, workspace=None,
                    stream=None):
     """Gradients of cross_attn_fwd for the same kv_len and key_mask; workspace: bwd_workspace_bytes."""
     import torch
-    c, device, a, n, m = _cross_args(p, (("q", q), ("k", k), ("v", v), ("o", o), ("dO", dO), ("dq", dq), ("dk", dk),
-                                         ("dv", dv)), kv_len, key_mask)
-    ls = _flat("lse", lse, p.q_shape[:3], torch.float32, device)
-    need = cross_query_sizes(p)["bwd_workspace_bytes"]
-    with _On(device, stream) as s:
-        _check(lib().llsa_cross_attn_bwd(ctypes.byref(c), a[0], a[1], a[2], n, m, a[3], a[4], ls, a[5], a[6], a[7],
-                                         _work(workspace, need, device), s), "cross_attn_bwd")
+    fixed, sizes, qs, ks, dt = _cross_of(p)
+    device = q.device
+    a = (_checked("q", q, qs, dt, device), _checked("k", k, ks, dt, device), _checked("v", v, ks, dt, device))
+    b = (_checked("o", o, qs, dt, device), _checked("dO", dO, qs, dt, device))
+    g = (_checked("dq", dq, qs, dt, device), _checked("dk", dk, ks, dt, device), _checked("dv", dv, ks, dt, device))
+    c = fixed + _PACK_CROSS(*_strides("q", q), *_strides("k", k), *_strides("v", v), *_strides("o", o),
+                            *_strides("dO", dO), *_strides("dq", dq), *_strides("dk", dk), *_strides("dv", dv))
+    n, m = _key_args(p, kv_len, key_mask, device)
+    ls = _flat("lse", lse, qs[:3], torch.float32, device)
+    _run(lib().llsa_cross_attn_bwd, "cross_attn_bwd", device, stream, c, *a, n, m, *b, ls, *g,
+         _work(workspace, sizes["bwd_workspace_bytes"], device))
 
 
 def _buffer(shape, dtype, device, token_major: bool):
@@ -615,55 +639,65 @@ def norm_query_sizes(p: NormProblem) -> dict:
     return {name: getattr(s, name) for name, _ in CNormBuffers._fields_}
 
 
-def _norm_args(p: NormProblem, named):
-    c = p.cp()
-    device = named[0][1].device
-    ptrs = []
-    for name, x in named:
-        if x is None:
-            ptrs.append(None)
-            continue
-        ptrs.append(_checked(name, x, p.shape, p.dtype, device))
-        _strided(name, getattr(c, name), x)
-    return c, device, ptrs
+@lru_cache(maxsize=256)
+def _norm_fixed(batch, heads, n, c, eps, dtype, param_dtype, per_batch):
+    """The C problem up to its strides, workspace bytes, shapes of rows and weights, their types."""
+    p = NormProblem(batch, heads, n, c, eps, dtype, param_dtype, per_batch)
+    need = norm_query_sizes(p)["bwd_workspace_bytes"]
+    return bytes(p.cp())[:_NORM_HEAD], need, p.shape, p.param_shape, _torch_dtype(dtype), _torch_dtype(param_dtype)
 
 
-def _param(p: NormProblem, c: CNormProblem, name: str, x, device):
-    """weight or bias: [c] contiguous, or [batch, c] with its rows apart by any stride."""
+def _norm_of(p: NormProblem):
+    return _norm_fixed(p.batch, p.heads, p.n, p.c, p.eps, p.dtype, p.param_dtype, p.per_batch)
+
+
+def _param(p: NormProblem, name: str, x, shape, dt, device):
+    """Address and row stride of weight or bias: [c] contiguous, or [batch, c] with its rows apart by any stride."""
     if x is None or isinstance(x, int):
-        return x
-    address = _checked(name, x, p.param_shape, p.param_dtype, device)
-    if p.per_batch:
-        if p.batch > 1 and x.stride(0) == 0:                # zero stands for contiguous rows
-            raise ValueError(f"{name}: one row expanded over the batch; per_batch=False takes it as [c]")
-        setattr(c, name + "_batch", x.stride(0) if p.batch > 1 else 0)
-    return address
+        return x, 0
+    address = _checked(name, x, shape, dt, device)
+    s = x.stride()
+    if s[-1] != 1 and p.c > 1:
+        raise ValueError(f"{name}: the last dimension is not contiguous")
+    if not p.per_batch or p.batch == 1:
+        return address, 0
+    if s[0] == 0:                                           # zero stands for contiguous rows
+        raise ValueError(f"{name}: one row expanded over the batch; per_batch=False takes it as [c]")
+    return address, s[0]
 
 
 def layer_norm_fwd(p: NormProblem, x, weight, bias, y, mean=None, rstd=None, stream=None):
-    """x, y: [batch, heads, n, c]; weight, bias: [c] (per_batch: [batch, c], rows any
-    stride apart) or None; mean, rstd: fp32 [batch, heads, n] or None."""
+    """x, y: [batch, heads, n, c]; weight, bias: [c] (per_batch: [batch, c], rows any stride apart) or None; mean,
+    rstd: fp32 [batch, heads, n] or None."""
     import torch
-    c, device, a = _norm_args(p, (("x", x), ("y", y)))
-    f = [_param(p, c, name, t, device) for name, t in (("weight", weight), ("bias", bias))]
-    st = [_flat(name, t, p.shape[:3], torch.float32, device) for name, t in (("mean", mean), ("rstd", rstd))]
-    with _On(device, stream) as s:
-        _check(lib().llsa_layer_norm_fwd(ctypes.byref(c), a[0], f[0], f[1], a[1], st[0], st[1], s), "layer_norm_fwd")
+    fixed, _, shape, pshape, dt, pt = _norm_of(p)
+    device = x.device
+    ax, ay = _checked("x", x, shape, dt, device), _checked("y", y, shape, dt, device)
+    w, ws = _param(p, "weight", weight, pshape, pt, device)
+    b, bs = _param(p, "bias", bias, pshape, pt, device)
+    c = fixed + _PACK_NORM(*_strides("x", x), *_strides("y", y), *_NO_STRIDES, *_NO_STRIDES, ws, bs)
+    f32 = torch.float32
+    _run(lib().llsa_layer_norm_fwd, "layer_norm_fwd", device, stream, c, ax, w, b, ay,
+         _flat("mean", mean, shape[:3], f32, device), _flat("rstd", rstd, shape[:3], f32, device))
 
 
 def layer_norm_bwd(p: NormProblem, x, dy, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None,
                    stream=None):
     """Gradients of layer_norm_fwd; dx, dweight and dbias are written where given; workspace: bwd_workspace_bytes."""
     import torch
-    c, device, a = _norm_args(p, (("x", x), ("dy", dy), ("dx", dx)))
-    pt = _torch_dtype(p.param_dtype)
-    f = [_param(p, c, "weight", weight, device)]
-    f += [_flat(name, t, p.param_shape, pt, device) for name, t in (("dweight", dweight), ("dbias", dbias))]
-    st = [_flat(name, t, p.shape[:3], torch.float32, device) for name, t in (("mean", mean), ("rstd", rstd))]
-    need = norm_query_sizes(p)["bwd_workspace_bytes"]
-    with _On(device, stream) as s:
-        _check(lib().llsa_layer_norm_bwd(ctypes.byref(c), a[0], a[1], f[0], st[0], st[1], a[2], f[1], f[2],
-                                         _work(workspace, need, device), s), "layer_norm_bwd")
+    fixed, need, shape, pshape, dt, pt = _norm_of(p)
+    device = x.device
+    ax, ag = _checked("x", x, shape, dt, device), _checked("dy", dy, shape, dt, device)
+    ad, sd = None, _NO_STRIDES
+    if dx is not None:
+        ad, sd = _checked("dx", dx, shape, dt, device), _strides("dx", dx)
+    w, ws = _param(p, "weight", weight, pshape, pt, device)
+    c = fixed + _PACK_NORM(*_strides("x", x), *_NO_STRIDES, *_strides("dy", dy), *sd, ws, 0)
+    f32 = torch.float32
+    _run(lib().llsa_layer_norm_bwd, "layer_norm_bwd", device, stream, c, ax, ag, w,
+         _flat("mean", mean, shape[:3], f32, device), _flat("rstd", rstd, shape[:3], f32, device), ad,
+         _flat("dweight", dweight, pshape, pt, device), _flat("dbias", dbias, pshape, pt, device),
+         _work(workspace, need, device))
 
 
 class LayerNorm:
