@@ -1,6 +1,7 @@
 // cross.cuh -- shared definitions of the cross-attention kernels.
 #pragma once
 
+#include "divisor.cuh"
 #include "llsa_internal.cuh"
 
 namespace llsa {

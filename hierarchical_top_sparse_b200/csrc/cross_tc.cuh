@@ -2,6 +2,7 @@
 #pragma once
 
 #include "cross.cuh"
+#include "packed.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -49,8 +50,63 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
+// A whole warp waits for a barrier, at most 2 s: all lanes ask, and go on or
+// give up together.  The vote before the branch keeps the ready case short
+// (about 70 cycles; a branch on each lane's own answer took about 190, and one
+// lane asking for all of them longer still).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (n & 63u) continue;
+    uint32_t now;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));    // (wraps after 4.3 s)
+    now = __shfl_sync(0xffffffffu, now, 0);
+    if (n == 64u) t0 = now;
+    if (now - t0 > 2000000000u) return false;
+  }
+}
+
+// The same for one lane.  (Neither is a call: a kernel that moves registers
+// between its warps cannot make one.)
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
+    if (n & 63u) continue;
+    uint32_t now;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+    if (n == 64u) t0 = now;
+    if (now - t0 > 2000000000u) return false;
+  }
+  return true;
+}
+
+// The registers of a thread, for all warps of a warpgroup at once.
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ void report(int* err, int code) {
   if (err) atomicExch(err, code);
+}
+
+// n / v.d, and n modulo v.d into rest.
+__device__ __forceinline__ int divide(int n, const Divisor& v, int& rest) {
+  const uint32_t q = over((uint32_t)n, v);
+  rest = (int)((uint32_t)n - q * v.d);
+  return (int)q;
 }
 
 // Bits of the 128 keys from key0 on that take part; lane i of the returned
@@ -62,6 +118,16 @@ __device__ __forceinline__ void key_bits(const uint8_t* mask, int key0, int n, i
     const bool ok = key < n && (!mask || mask[key]);
     bits[i] = __ballot_sync(0xffffffffu, ok);
   }
+}
+
+// The bits of a half of the keys: 16 * units from column col0 (16 * units or 0) on.
+__device__ __forceinline__ uint64_t half_bits(const uint8_t* mask, int key0, int n, int lane, uint32_t col0,
+                                              int units) {
+  uint32_t w[4];
+  key_bits(mask, key0, n, lane, w);
+  const uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
+  const uint64_t bits = col0 == 0 ? lo : (col0 == 64 ? hi : (lo >> col0) | (hi << (64 - col0)));
+  return units >= 4 ? bits : bits & ((1ull << (16 * units)) - 1);
 }
 
 // Zeros the rows of a swizzled [128][64 x panels] tile whose bit is clear
@@ -122,6 +188,61 @@ __device__ __forceinline__ void store16(const float* f, __nv_bfloat16* out, floa
       d4[3] = make_float4(f[12], f[13], f[14], f[15]);
     }
   }
+}
+
+// Result rows on their way out: the four epilogue warps write a panel of 128
+// rows and 64 channels in shared memory and one thread sends it by TMA, which
+// clips rows and channels behind the ends.  (Each thread storing its own row
+// takes 32 lines an instruction, and everything else that uses the memory
+// pipe, mbarriers and tensor-memory loads among it, queues behind.)
+struct Outgoing {
+  alignas(1024) unsigned char tile[kPanel];
+  alignas(8) uint64_t full, free;
+};
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int n, int h, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(n), "r"(h), "r"(b), "r"(ptx::smem_u32(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// One panel: values(c, f) gives this thread's 16 values from column 16 c of the
+// panel on; `count` panels went before; wait(barrier, parity) as in the kernels.
+// False when a wait ran out.
+template <typename Values, typename Wait>
+__device__ __forceinline__ bool send_panel(Outgoing& o, uint32_t count, bool leader, int lane, int row,
+                                           const CUtensorMap* map, int x, int n, int h, int b, bool any, Values values,
+                                           Wait wait) {
+  if (count > 0) {
+    if (leader && lane == 0) {
+      tma_stores_read();
+      ptx::mbar_arrive(&o.free);
+    }
+    __syncwarp();
+    if (!wait(&o.free, (count - 1) & 1)) return false;
+  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float f[16];
+    values(c, f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<uint4*>(o.tile + row * 128 + (((2 * c + e) ^ (row & 7)) << 4)) =
+          make_uint4(ptx::pack_bf16(f[8 * e], f[8 * e + 1]), ptx::pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                     ptx::pack_bf16(f[8 * e + 4], f[8 * e + 5]), ptx::pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+  }
+  ptx::fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(&o.full);
+  __syncwarp();
+  if (!leader) return true;
+  if (!wait(&o.full, count & 1)) return false;
+  if (lane == 0 && any) tma_store_4d(map, o.tile, x, n, h, b);
+  __syncwarp();
+  return true;
 }
 
 inline int sm_count() {

@@ -40,6 +40,7 @@ struct Args {
   Where wq, wk, wv, wg;
   int packed, qs, nqt, units, tiles;           // query splits, query tiles per head and per key head, key tiles
   int items;
+  Divisor by_qs, by_tiles, by_hk, by_nqt, by_nq;
   const void *q, *dO;
   const float *lse, *D;
   void *dk, *dv;
@@ -68,10 +69,8 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const Args& a, int it) {
   Item x;
-  x.split = it % a.qs;
-  const int tile = (it / a.qs) % a.tiles, slice = it / a.qs / a.tiles;
-  x.b = slice / a.g.hk;
-  x.hk = slice % a.g.hk;
+  int tile;
+  x.b = divide(divide(divide(it, a.by_qs, x.split), a.by_tiles, tile), a.by_hk, x.hk);
   x.len = key_count(a.g, a.keys, x.b);
   x.key0 = tile * kTile;
   x.u0 = (int)((int64_t)a.units * x.split / a.qs);
@@ -82,17 +81,19 @@ __device__ __forceinline__ Item item_of(const Args& a, int it) {
 __device__ __forceinline__ bool row_of(const Args& a, int hk, int u, int r, int& h, int& n) {
   if (a.packed) {
     const int rr = u * kTile + r;
-    h = hk * a.g.group + rr / a.g.nq;
-    n = rr % a.g.nq;
+    h = hk * a.g.group + divide(rr, a.by_nq, n);
     return rr < a.g.group * a.g.nq;
   }
-  h = hk * a.g.group + u / a.nqt;
-  n = (u % a.nqt) * kTile + r;
+  int tile;
+  h = hk * a.g.group + divide(u, a.by_nqt, tile);
+  n = tile * kTile + r;
   return n < a.g.nq;
 }
 // Columns of query tile u that are computed: its rows, rounded up to 32.
 __device__ __forceinline__ int tile_cols(const Args& a, int u) {
-  const int left = a.packed ? a.g.group * a.g.nq - u * kTile : a.g.nq - (u % a.nqt) * kTile;
+  int tile = u;
+  if (!a.packed) divide(u, a.by_nqt, tile);
+  const int left = (a.packed ? a.g.group * a.g.nq : a.g.nq) - tile * kTile;
   return left >= kTile ? kTile : (left + 31) & ~31;
 }
 
@@ -144,7 +145,7 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
   // Every lane of a warp waits, and all go on together or all give up together.
   auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
     if (!ok) return false;
-    ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+    ok = warp_wait(bar, parity);
     if (!ok && lane == 0) report(a.err, code);
     return ok;
   };
@@ -297,7 +298,9 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         for (int i = 0; i < x.n && !a.packed; ++i) {
           const uint32_t st = tc_ % ST;
           if (!wait1(&s.empty[st], ((tc_ / ST) & 1) ^ 1, 144)) break;
-          const int u = x.u0 + i, h = x.hk * g.group + u / a.nqt, n0 = (u % a.nqt) * kTile;
+          int n0;
+          const int h = x.hk * g.group + divide(x.u0 + i, a.by_nqt, n0);
+          n0 *= kTile;
           ptx::mbar_arrive_expect_tx(&s.full[st], 2 * kBytes);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
@@ -456,6 +459,11 @@ cudaError_t launch_bwd_kv(const Geo& g, const DkvPlan& p, const CUtensorMap* t, 
   a.units = p.units;
   a.tiles = p.tiles;
   a.items = (int)p.items;
+  a.by_qs = divisor(p.qs);
+  a.by_tiles = divisor(p.tiles);
+  a.by_hk = divisor(g.hk);
+  a.by_nqt = divisor(p.nqt);
+  a.by_nq = divisor(g.nq);
   a.q = q;
   a.dO = dO;
   a.lse = lse;

@@ -31,6 +31,7 @@ struct Args {
   Where wq, wk, wv, wg;
   int packed, ks, ct, tiles;                   // key splits, key tiles per split, query tiles per slice
   int items;
+  Divisor by_ks, by_tiles, by_heads, by_group, by_nq;
   const void *q, *dO;
   const float *lse, *D;
   void* dq;
@@ -57,12 +58,10 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const Args& a, int it) {
   Item x;
-  x.split = it % a.ks;
-  const int tile = (it / a.ks) % a.tiles, slice = it / a.ks / a.tiles;
-  const int per = a.packed ? a.g.hk : a.g.h;
-  x.b = slice / per;
-  x.h = a.packed ? (slice % per) * a.g.group : slice % per;
-  x.hk = x.h / a.g.group;
+  int tile, h;
+  x.b = divide(divide(divide(it, a.by_ks, x.split), a.by_tiles, tile), a.by_heads, h);
+  x.h = a.packed ? h * a.g.group : h;
+  x.hk = a.packed ? h : over(h, a.by_group);
   x.rows = a.packed ? a.g.group * a.g.nq : a.g.nq;
   x.row0 = tile * kTile;
   x.len = key_count(a.g, a.keys, x.b);
@@ -78,8 +77,9 @@ __device__ __forceinline__ int tile_cols(const Item& x, int j) {
 // Row r of the item: head and token; false behind the last row.
 __device__ __forceinline__ bool row_of(const Args& a, const Item& x, int r, int& h, int& n) {
   const int rr = x.row0 + r;
-  h = a.packed ? x.h + rr / a.g.nq : x.h;
-  n = a.packed ? rr % a.g.nq : rr;
+  h = x.h;
+  n = rr;
+  if (a.packed) h += divide(rr, a.by_nq, n);
   return rr < x.rows;
 }
 
@@ -132,7 +132,7 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
   // Every lane of a warp waits, and all go on together or all give up together.
   auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
     if (!ok) return false;
-    ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+    ok = warp_wait(bar, parity);
     if (!ok && lane == 0) report(a.err, code);
     return ok;
   };
@@ -472,6 +472,11 @@ cudaError_t launch_bwd_q(const Geo& g, const DqPlan& p, const CUtensorMap* t, co
   a.ct = p.ct;
   a.tiles = p.tiles;
   a.items = (int)p.items;
+  a.by_ks = divisor(p.ks);
+  a.by_tiles = divisor(p.tiles);
+  a.by_heads = divisor(p.packed ? g.hk : g.h);
+  a.by_group = divisor(g.group);
+  a.by_nq = divisor(g.nq);
   a.q = q;
   a.dO = dO;
   a.lse = lse;

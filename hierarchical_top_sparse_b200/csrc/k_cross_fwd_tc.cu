@@ -11,7 +11,7 @@
 // The maximum is lazy: O (in TMEM) is rescaled only when a logit exceeds m by
 // more than 2^8, so weights stay below 256.  The bound is the exponential (16
 // a cycle and SM): the two tiles of an item run on warpgroups of their own, so
-// that one tile's products hide behind the other's exponentials.
+// that one works while the other waits.
 //
 // Rows: the tokens of one query head, or, where a head has fewer than 128, the
 // tokens of all heads of a key head, one after the other (each key head's keys
@@ -23,8 +23,8 @@
 // cleared in shared memory, so that 0 * V is 0 whatever V holds.
 //
 // Warps (one CTA per SM, items dealt round robin): 0-3 and 4-7 softmax of tile
-// 0 and 1, 8-11 epilogue, 12 producer (TMA), 13 and 14 MMA issue of tile 0 and
-// 1, 15 clears rows of V; warp 15 also gathers Q where heads are packed.
+// 0 and 1, 8-11 epilogue, 12 producer (TMA), 13 MMA issue of S, 14 of O, 15
+// clears rows of V, and gathers Q where heads are packed.
 // Up to 64 channels, P has columns of its own and S of the next key tile is
 // computed while P of this one is made; above, P takes S's columns.
 #include <math.h>
@@ -39,18 +39,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kHeadroom = 8.f;               // log2 of the largest weight before O is rescaled
 constexpr int THREADS = 512;
-constexpr int EPI0 = 8, PRODUCER = 12, MMA0 = 13, FIXER = 15;
+constexpr int EPI0 = 8, PRODUCER = 12, MMA_S = 13, FIXER = 15;
 constexpr uint32_t TMEM_COLS = 512;
+// Registers of a thread: at launch, then of the softmax warps and of the others.  (A share that the block was not
+// launched with would be waited for without end.)
+constexpr int REGS = 65536 / THREADS / 8 * 8, SOFT_REGS = 184, OTHER_REGS = 72;
+static_assert(EPI0 * 32 * SOFT_REGS + (THREADS - EPI0 * 32) * OTHER_REGS <= THREADS * REGS, "register shares");
 
 struct Args {
   Geo g;
   Keys keys;
   Where wq, wk, wv;
   int ks, ct;                                  // key splits, key tiles per split
-  int tpi;                                     // query tiles per item: 1 or 2
+  int tpi;                                     // query tiles per item: 1, or 2 (the last of a slice may be empty)
   int packed;                                  // rows: all heads of a key head
   int slices, pairs;                           // slices of rows; items' row groups per slice
   int items;
+  Divisor by_ks, by_pairs, by_heads, by_group, by_nq;    // heads: of a batch row's slices
   const void* q;                               // where heads are packed
   void* o;
   float* lse;
@@ -64,6 +69,7 @@ struct Smem {
   alignas(1024) unsigned char q[2][QST][NP * kPanel];
   alignas(1024) unsigned char k[NS][NP * kPanel];
   alignas(1024) unsigned char v[NS][NP * kPanel];
+  Outgoing out;
   float stat_m[2][128], stat_l[2][128];        // an item's row maxima and sums: softmax -> epilogue
   alignas(8) uint64_t qfull[2][QST], qempty[2][QST];
   uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], vready[NS];
@@ -79,17 +85,16 @@ struct Item {
 
 __device__ __forceinline__ Item item_of(const Args& a, int it) {
   Item x;
-  x.split = it % a.ks;
-  const int p = (it / a.ks) % a.pairs, slice = it / a.ks / a.pairs;
+  int p, h;
+  const int slice = divide(divide(it, a.by_ks, x.split), a.by_pairs, p);
+  x.b = divide(slice, a.by_heads, h);
   if (a.packed) {
-    x.b = slice / a.g.hk;
-    x.hk = slice % a.g.hk;
-    x.h = x.hk * a.g.group;
+    x.hk = h;
+    x.h = h * a.g.group;
     x.rows = a.g.group * a.g.nq;
   } else {
-    x.b = slice / a.g.h;
-    x.h = slice % a.g.h;
-    x.hk = x.h / a.g.group;
+    x.h = h;
+    x.hk = over(h, a.by_group);
     x.rows = a.g.nq;
   }
   x.row0 = p * a.tpi * kTile;
@@ -100,9 +105,6 @@ __device__ __forceinline__ Item item_of(const Args& a, int it) {
   x.n = max(t1 - t0, 0);
   x.key0 = t0 * kTile;
   return x;
-}
-__device__ __forceinline__ bool tile_active(const Args& a, const Item& x, int t) {
-  return t < a.tpi && x.row0 + t * kTile < x.rows;
 }
 // Columns of a key tile that are computed: its keys up to the length, rounded up to 32.
 __device__ __forceinline__ int tile_cols(const Item& x, int j) {
@@ -122,7 +124,8 @@ template <int NP>
 __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constant__ Args a,
                                                             const __grid_constant__ CUtensorMap tq,
                                                             const __grid_constant__ CUtensorMap tk,
-                                                            const __grid_constant__ CUtensorMap tv) {
+                                                            const __grid_constant__ CUtensorMap tv,
+                                                            const __grid_constant__ CUtensorMap to) {
   using S = Smem<NP>;
   constexpr int QST = S::QST, NS = S::NS;
   constexpr uint32_t kBytes = NP * kPanel;
@@ -147,11 +150,13 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
     }
     for (int i = 0; i < NS; ++i) {
       ptx::mbar_init(&s.kfull[i], 1);
-      ptx::mbar_init(&s.kempty[i], 2);
+      ptx::mbar_init(&s.kempty[i], 1);
       ptx::mbar_init(&s.vfull[i], 1);
-      ptx::mbar_init(&s.vempty[i], 2);
+      ptx::mbar_init(&s.vempty[i], 1);
       ptx::mbar_init(&s.vready[i], 1);
     }
+    ptx::mbar_init(&s.out.full, 4);
+    ptx::mbar_init(&s.out.free, 1);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -170,21 +175,23 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
   // Every lane of a warp waits, and all go on together or all give up together.
   auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
     if (!ok) return false;
-    ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+    ok = warp_wait(bar, parity);
     if (!ok && lane == 0) report(a.err, code);
     return ok;
   };
 
-  if (warp < 8) {
-    // ============================================================ softmax
+  if (warp < EPI0) {
+    // ============================================================ softmax: one row a thread
+    more_registers<SOFT_REGS>();
     const int t = warp >> 2, sub = warp & 3;
+    const int items = t < a.tpi ? a.items : 0;
     const int row = sub * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)(sub * 32) << 16);
     const float sc2 = g.scale * kLog2e;        // logits in the log2 domain
+    const f2 scale2 = twice(sc2);
     uint32_t sc = 0, oc = 0;
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const Item x = item_of(a, it);
-      if (!tile_active(a, x, t)) continue;
       const uint8_t* mask = a.keys.mask ? a.keys.mask + (int64_t)x.b * g.nk : nullptr;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < x.n; ++j, ++sc) {
@@ -195,19 +202,28 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         if (!whole) key_bits(mask, key0, x.len, lane, bits);
         if (!wait(&s.s_full[t], sc & 1, 91)) break;
         tc::fence_after_sync();
-        float mx = -INFINITY;
+        // the whole row of S in registers (columns behind `blocks` hold anything: their bits are clear)
+        uint32_t r[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < blocks) {
-            uint32_t r[32];
-            tmem_ld32(tl + col_s(t) + 32u * c, r);
-            tc::tmem_wait_ld();
-            if (!whole) keep_keys(r, bits[c]);
-            float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int c = 0; c < 4; ++c) tmem_ld32(tl + col_s(t) + 32u * c, r + 32 * c);
+        tc::tmem_wait_ld();
+        if (NP == 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&s.s_empty[t]);
+          __syncwarp();
+        }
+        if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i & 3] = fmaxf(y[i & 3], __uint_as_float(r[i]));
-            mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-          }
+          for (int c = 0; c < 4; ++c) keep_keys(r + 32 * c, bits[c]);
+        }
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaxf(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+#pragma unroll
+        for (int i = 16; i < 128; i += 2)
+          y[(i >> 1) & 7] = max3(y[(i >> 1) & 7], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+        const float mx = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
         const float mn = fmaxf(m, mx * sc2);
         bool resc = false;
         float f = 1.f;
@@ -219,11 +235,10 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           m = mn;
           l *= f;
         }
-        const float ref = m == -INFINITY ? 0.f : m;    // no key so far: every weight is 2^-inf = 0
-        // the O update of the tile before has read P and is in O
-        if (!wait(&s.p_empty[t], (sc & 1) ^ 1, 92)) break;
-        tc::fence_after_sync();
+        const float ref = m == -INFINITY ? 0.f : m;      // no key so far: every weight is 2^-inf = 0
         if (__any_sync(0xffffffffu, resc)) {
+          if (!wait(&s.p_empty[t], (sc & 1) ^ 1, 92)) break;     // every earlier update is in O
+          tc::fence_after_sync();
           const int oc16 = (g.d + 15) >> 4;
 #pragma unroll 1
           for (int c = 0; c < oc16; ++c) {
@@ -235,70 +250,74 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
             tc::tmem_st16(tl + col_o(t) + 16u * c, w);
           }
         }
-        // S once more (it costs less than registers for 128 logits), the next 32 columns on their way
-        float l0 = 0.f, l1 = 0.f;
-        uint32_t r[2][32];
-        tmem_ld32(tl + col_s(t), r[0]);
-        tc::tmem_wait_ld();
+        const f2 ref2 = twice(-ref);
+        f2 sum = twice(0.f);
+        auto weights = [&](int c, uint32_t* w) {         // of 32 keys
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < blocks) {
-            if (c + 1 < blocks) {
-              tmem_ld32(tl + col_s(t) + 32u * (c + 1), r[(c + 1) & 1]);
-            } else if (NP == 1) {
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(&s.s_empty[t]);
-              __syncwarp();
-            }
-            if (!whole) keep_keys(r[c & 1], bits[c]);
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float p0 = ptx::ex2(fmaf(__uint_as_float(r[c & 1][2 * i]), sc2, -ref));
-              const float p1 = ptx::ex2(fmaf(__uint_as_float(r[c & 1][2 * i + 1]), sc2, -ref));
-              l0 += p0;
-              l1 += p1;
-              w[i] = ptx::pack_bf16(p0, p1);
-            }
-            tc::tmem_wait_ld();
-            tc::tmem_st16(tl + col_p(t) + 16u * c, w);
+          for (int i = 0; i < 16; ++i) {
+            float p0, p1;
+            split(fma2(pair(__uint_as_float(r[32 * c + 2 * i]), __uint_as_float(r[32 * c + 2 * i + 1])), scale2, ref2),
+                  p0, p1);
+            p0 = ptx::ex2(p0);
+            p1 = ptx::ex2(p1);
+            sum = add2(sum, pair(p0, p1));
+            w[i] = ptx::pack_bf16(p0, p1);
           }
-        l += l0 + l1;
+        };
+        // the first half of the weights before P is free: the O update of the tile before is still reading it
+        uint32_t w0[16], w1[16];
+        weights(0, w0);
+        if (1 < blocks) weights(1, w1);
+        if (!wait(&s.p_empty[t], (sc & 1) ^ 1, 92)) break;
+        tc::fence_after_sync();
+        tc::tmem_st16(tl + col_p(t), w0);
+        if (1 < blocks) tc::tmem_st16(tl + col_p(t) + 16u, w1);
+        if (2 < blocks) {
+          weights(2, w0);
+          tc::tmem_st16(tl + col_p(t) + 32u, w0);
+        }
+        if (3 < blocks) {
+          weights(3, w1);
+          tc::tmem_st16(tl + col_p(t) + 48u, w1);
+        }
+        l += both(sum);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&s.p_full[t]);
+        __syncwarp();
       }
       if (!wait(&s.o_empty[t], (oc & 1) ^ 1, 93)) break;    // the epilogue has read the last item's statistics
       s.stat_m[t][row] = m;
       s.stat_l[t][row] = l;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&s.st_full[t]);
+      __syncwarp();
       ++oc;
     }
   } else {
+    fewer_registers<OTHER_REGS>();
     if (warp < EPI0 + 4) {
       // ============================================================ epilogue
       const int sub = warp & 3;
       const uint32_t tl = tbase + ((uint32_t)(sub * 32) << 16);
-      uint32_t oc[2] = {0, 0};
+      uint32_t oc[2] = {0, 0}, sent = 0;
+      const bool direct = a.packed || a.ks > 1;    // rows that TMA cannot place, or fp32 parts
       for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
         const Item x = item_of(a, it);
 #pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          if (!tile_active(a, x, t)) continue;
+        for (int t = 0; t < a.tpi; ++t) {
           const uint32_t c0 = t ? oc[1] : oc[0];
           if (t) ++oc[1]; else ++oc[0];
           if (!wait(&s.st_full[t], c0 & 1, 94) || !wait(&s.o_full[t], c0 & 1, 94)) break;
           tc::fence_after_sync();
-          const float m = s.stat_m[t][sub * 32 + lane], l = s.stat_l[t][sub * 32 + lane];
+          const float m = s.stat_m[t][sub * 32 + lane];
+          const float l = s.stat_l[t][sub * 32 + lane];
           const int r = x.row0 + t * kTile + sub * 32 + lane;
           const bool live = r < x.rows;
           int h = x.h, n = r;
           if (a.packed && live) {
-            h = x.h + r / g.nq;
-            n = r % g.nq;
+            h = x.h + divide(r, a.by_nq, n);
           }
           const bool none = m == -INFINITY && !(l > 0.f) && l == l;    // NaN sums pass through
           const float inv = none ? 0.f : 1.f / l;
@@ -306,17 +325,30 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           const int64_t at = ((int64_t)x.b * g.h + h) * g.nq + n;
           __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.o) + x.b * g.o.b + h * g.o.h + n * g.o.n;
           float* pp = a.part.o + ((int64_t)x.split * rows_of(g) + at) * g.d;
-          const int c16 = (g.d + 15) >> 4;
-#pragma unroll 1
-          for (int c = 0; c < c16; ++c) {
+          auto values = [&](int col, float* f) {
             uint32_t w[16];
-            tc::tmem_ld16(tl + col_o(t) + 16u * c, w);
+            tc::tmem_ld16(tl + col_o(t) + col, w);
             tc::tmem_wait_ld();
-            float f[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : __uint_as_float(w[i]) * inv;
-            if (live) store16(f, a.ks > 1 ? nullptr : po + 16 * c, pp + 16 * c, 16 * c + 8 < g.d);
-            __syncwarp();
+            for (int e = 0; e < 16; ++e) f[e] = none ? 0.f : __uint_as_float(w[e]) * inv;
+          };
+          if (direct) {
+#pragma unroll 1
+            for (int c = 0; c < g.d; c += 16) {
+              float f[16];
+              values(c, f);
+              if (live) store16(f, a.ks > 1 ? nullptr : po + c, pp + c, c + 8 < g.d);
+              __syncwarp();
+            }
+          } else {
+            const int n0 = x.row0 + t * kTile;
+#pragma unroll 1
+            for (int p = 0; p < NP; ++p, ++sent)
+              if (!send_panel(s.out, sent, warp == EPI0, lane, sub * 32 + lane, &to, 64 * p, n0, x.h, x.b, n0 < x.rows,
+                              [&](int c, float* f) { values(64 * p + 16 * c, f); },
+                              [&](uint64_t* bar, uint32_t parity) { return wait(bar, parity, 100); }))
+                break;
+            if (!ok) break;
           }
           if (live) {
             if (a.ks > 1)
@@ -329,12 +361,15 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           if (lane == 0) ptx::mbar_arrive(&s.o_empty[t]);
         }
       }
+      if (warp == EPI0 && lane == 0) tma_stores_done();
+      __syncwarp();
     } else if (warp == PRODUCER) {
       // ============================================================ producer
       uint32_t qc[2] = {0, 0}, kc = 0;
+      bool k_alone = false;                    // a K was asked for, its V not yet
       if (lane == 0) {
         auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-          if (ok && !ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
+          if (ok && !lane_wait(bar, parity)) {
             ok = false;
             report(a.err, code);
           }
@@ -344,8 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           const Item x = item_of(a, it);
           if (x.n == 0) continue;
 #pragma unroll 1
-          for (int t = 0; t < 2 && !a.packed; ++t) {
-            if (!tile_active(a, x, t)) continue;
+          for (int t = 0; t < a.tpi && !a.packed; ++t) {
             const uint32_t c = qc[t];
             uint64_t* full = &s.qfull[t][c % QST];
             if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 95)) break;
@@ -364,7 +398,9 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
             for (int p = 0; p < NP; ++p)
               tma_load_4d(s.k[i] + p * kPanel, &tk, 64 * p, x.key0 + j * kTile, x.hk * a.wk.h, x.b * a.wk.b,
                           &s.kfull[i]);
+            k_alone = true;
             if (!wait(&s.vempty[i], ph, 96)) break;
+            k_alone = false;
             ptx::mbar_arrive_expect_tx(&s.vfull[i], kBytes);
 #pragma unroll
             for (int p = 0; p < NP; ++p)
@@ -377,12 +413,12 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         if (!ok) {
           for (int t = 0; t < 2 && !a.packed; ++t)
             for (uint32_t c = qc[t] > QST ? qc[t] - QST : 0; c < qc[t]; ++c)
-              ptx::mbar_wait_bounded(&s.qfull[t][c % QST], (c / QST) & 1, kWaitLimitNs);
+              lane_wait(&s.qfull[t][c % QST], (c / QST) & 1);
           for (uint32_t c = kc > NS ? kc - NS : 0; c < kc; ++c) {
-            ptx::mbar_wait_bounded(&s.kfull[c % NS], (c / NS) & 1, kWaitLimitNs);
-            ptx::mbar_wait_bounded(&s.vfull[c % NS], (c / NS) & 1, kWaitLimitNs);
+            lane_wait(&s.kfull[c % NS], (c / NS) & 1);
+            lane_wait(&s.vfull[c % NS], (c / NS) & 1);
           }
-          ptx::mbar_wait_bounded(&s.kfull[kc % NS], (kc / NS) & 1, 1000000ull);   // a K without its V
+          if (k_alone) lane_wait(&s.kfull[kc % NS], (kc / NS) & 1);
         }
       }
       __syncwarp();
@@ -394,15 +430,13 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         if (x.n == 0) continue;
         if (a.packed) {
 #pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            if (!tile_active(a, x, t)) continue;
+          for (int t = 0; t < a.tpi; ++t) {
             const uint32_t c = qc[t]++;
             if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 97)) break;
             gather_rows<NP>(s.q[t][c % QST], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane,
                             [&](int r, int& h, int& n) {
                               const int rr = x.row0 + t * kTile + r;
-                              h = x.h + rr / g.nq;
-                              n = rr % g.nq;
+                              h = x.h + divide(rr, a.by_nq, n);
                               return rr < x.rows;
                             });
             ptx::fence_proxy_async();
@@ -428,84 +462,80 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         }
       }
     } else {
-      // ============================================================ MMA issue of tile t
-      const int t = warp - MMA0;
+      // ============================================================ MMA issue: one warp S, one O
+      const bool is_s = warp == MMA_S;
       const uint64_t dk0 = tc::sw128_desc(ptx::smem_u32(s.k[0]), 16, 1024);
       const uint64_t dv0 = tc::sw128_desc(ptx::smem_u32(s.v[0]), kPanel, 1024);
-      const uint64_t dq0 = tc::sw128_desc(ptx::smem_u32(s.q[t][0]), 16, 1024);
+      const uint64_t dq0 = tc::sw128_desc(ptx::smem_u32(s.q[0][0]), 16, 1024);
+      constexpr uint64_t kStep = kBytes >> 4;
       const int dsteps = (g.d + 15) >> 4;
       const uint32_t id_o = tc::idesc_bf16(128, 16 * dsteps, 0, 1);      // O += P V: A = P (TMEM), B = V (MN-major)
-      uint32_t kc = 0, sc = 0, qc = 0, oc = 0;
-      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+      uint32_t kc = 0, qc = 0, oc = 0;         // key tiles, items with keys, items
+      for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x, ++oc) {
         const Item x = item_of(a, it);
-        if (!tile_active(a, x, t)) {           // the other tile's keys pass by
-          for (int j = 0; j < x.n && ok; ++j, ++kc) {
-            const uint32_t i = kc % NS, ph = (kc / NS) & 1;
-            if (!wait(&s.kfull[i], ph, 99)) break;
-            if (lane == 0) ptx::mbar_arrive(&s.kempty[i]);
-            if (!wait(&s.vready[i], ph, 99)) break;
-            if (lane == 0) ptx::mbar_arrive(&s.vempty[i]);
+        if (x.n == 0) {                        // no keys: O is not there, the epilogue goes on
+          for (int t = 0; t < a.tpi && !is_s; ++t) {
+            if (!wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) break;
+            if (tc::elect_one()) tc::commit(&s.o_full[t]);
+            __syncwarp();
           }
           continue;
         }
-        auto issue_s = [&](int j) {
-          const uint32_t c = kc + j, i = c % NS;
-          if (!wait(&s.kfull[i], (c / NS) & 1, 99)) return;
-          // NP == 1: the softmax has read the last S; NP == 2: the O update has read P from these columns
-          if (!wait(NP == 1 ? &s.s_empty[t] : &s.p_empty[t], ((sc + j) & 1) ^ 1, 99)) return;
-          tc::fence_after_sync();
-          const uint32_t id = tc::idesc_bf16(128, tile_cols(x, j), 0, 0);
-          const uint64_t qd = dq0 + (uint64_t)(qc % QST) * (kBytes >> 4), kd = dk0 + (uint64_t)i * (kBytes >> 4);
-          if (tc::elect_one()) {
-            for (int k = 0; k < dsteps; ++k) {
-              const uint64_t o = (uint64_t)(k >> 2) * (kPanel >> 4) + 2u * (k & 3);
-              tc::mma_bf16(tbase + col_s(t), qd + o, kd + o, id, k > 0);
+        for (int j = 0; j < x.n && ok; ++j, ++kc) {
+          const uint32_t i = kc % NS, ph = kc & 1;
+          const int cols = tile_cols(x, j);
+          if (!wait(is_s ? &s.kfull[i] : &s.vready[i], (kc / NS) & 1, 99)) break;
+          if (is_s) {
+            const uint32_t id = tc::idesc_bf16(128, cols, 0, 0);
+#pragma unroll 1
+            for (int t = 0; t < a.tpi; ++t) {
+              const uint32_t qs = qc % QST;
+              if (j == 0 && !wait(&s.qfull[t][qs], (qc / QST) & 1, 99)) break;
+              // NP == 1: the softmax has read the last S; NP == 2: the O update has read P from these columns
+              if (!wait(NP == 1 ? &s.s_empty[t] : &s.p_empty[t], ph ^ 1, 99)) break;
+              tc::fence_after_sync();
+              const uint64_t qd = dq0 + (t * QST + qs) * kStep, kd = dk0 + i * kStep;
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4 * NP; ++k)
+                  if (k < dsteps) {
+                    const uint64_t o = (uint64_t)(k >> 2) * (kPanel >> 4) + 2u * (k & 3);
+                    tc::mma_bf16(tbase + col_s(t), qd + o, kd + o, id, k > 0);
+                  }
+                tc::commit(&s.s_full[t]);
+                if (j == x.n - 1) tc::commit(&s.qempty[t][qs]);
+                if (t == a.tpi - 1) tc::commit(&s.kempty[i]);
+              }
+              __syncwarp();
             }
-            tc::commit(&s.s_full[t]);
-            tc::commit(&s.kempty[i]);
-            if (j == x.n - 1) tc::commit(&s.qempty[t][qc % QST]);
+          } else {
+            const int steps = cols >> 4;
+#pragma unroll 1
+            for (int t = 0; t < a.tpi; ++t) {
+              if (!wait(&s.p_full[t], ph, 99)) break;
+              if (j == 0 && !wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) break;   // the last item's O has been read
+              tc::fence_after_sync();
+              const uint64_t vd = dv0 + i * kStep;
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)    // 16 keys: 8 columns of P, 2 KB of V's panel
+                  if (k < steps)
+                    tc::mma_bf16_ta(tbase + col_o(t),
+                                    tbase + col_p(t) + 8u * k, vd + 128u * k, id_o, j > 0 || k > 0);
+                tc::commit(&s.p_empty[t]);
+                if (j == x.n - 1) tc::commit(&s.o_full[t]);
+                if (t == a.tpi - 1) tc::commit(&s.vempty[i]);
+              }
+              __syncwarp();
+            }
           }
-          __syncwarp();
-        };
-        auto issue_o = [&](int j) {
-          const uint32_t c = kc + j, i = c % NS;
-          if (!wait(&s.vready[i], (c / NS) & 1, 99)) return;
-          if (!wait(&s.p_full[t], (sc + j) & 1, 99)) return;
-          if (j == 0 && !wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) return;    // the last item's O has been read
-          tc::fence_after_sync();
-          const int steps = (tile_cols(x, j)) >> 4;
-          const uint64_t vd = dv0 + (uint64_t)i * (kBytes >> 4);
-          if (tc::elect_one()) {
-            for (int k = 0; k < steps; ++k)    // 16 keys: 8 columns of P, 2 KB of V's panel
-              tc::mma_bf16_ta(tbase + col_o(t), tbase + col_p(t) + 8u * k, vd + 128u * k, id_o, j > 0 || k > 0);
-            tc::commit(&s.p_empty[t]);
-            tc::commit(&s.vempty[i]);
-          }
-          __syncwarp();
-        };
-        if (x.n > 0) {
-          if (!wait(&s.qfull[t][qc % QST], (qc / QST) & 1, 99)) break;
-          issue_s(0);
-          for (int j = 0; j < x.n && ok; ++j) {
-            if (NP == 1 && j + 1 < x.n) issue_s(j + 1);
-            if (ok) issue_o(j);
-            if (NP == 2 && ok && j + 1 < x.n) issue_s(j + 1);
-          }
-          kc += x.n;
-          sc += x.n;
-          ++qc;
-        } else if (!wait(&s.o_empty[t], (oc & 1) ^ 1, 99)) {
-          break;
         }
-        if (!ok) break;
-        if (tc::elect_one()) tc::commit(&s.o_full[t]);
-        __syncwarp();
-        ++oc;
+        ++qc;
       }
       // every MMA issued here has finished before TMEM is released
-      if (tc::elect_one()) tc::commit(&s.drain[t]);
+      if (tc::elect_one()) tc::commit(&s.drain[is_s]);
       __syncwarp();
-      ptx::mbar_wait_bounded(&s.drain[t], 0, kWaitLimitNs);
+      warp_wait(&s.drain[is_s], 0);
     }
   }
   tc::fence_before_sync();
@@ -550,12 +580,12 @@ TcPlan plan_fwd_tc(const Geo& g, int sms) {
 
 template <int NP>
 static cudaError_t launch(const fwdtc::Args& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int grid, cudaStream_t s) {
+                          const CUtensorMap& to, int grid, cudaStream_t s) {
   const size_t smem = sizeof(fwdtc::Smem<NP>) + 1024;
   cudaError_t e =
       cudaFuncSetAttribute(fwdtc::fwd_tc_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  fwdtc::fwd_tc_kernel<NP><<<grid, fwdtc::THREADS, smem, s>>>(a, tq, tk, tv);
+  fwdtc::fwd_tc_kernel<NP><<<grid, fwdtc::THREADS, smem, s>>>(a, tq, tk, tv, to);
   note_launches(1);
   return cudaGetLastError();
 }
@@ -563,10 +593,12 @@ static cudaError_t launch(const fwdtc::Args& a, const CUtensorMap& tq, const CUt
 cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
                           const Keys& keys, void* o, float* lse, void* work, cudaStream_t s) {
   fwdtc::Args a;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
+  Where whole;                                 // a result repeats nothing: its coordinates are all its own
   cudaError_t e = make_map4(&tq, &a.wq, q, g.q, g.h, g.b, g.nq, g.d, kTile);
   if (e == cudaSuccess) e = make_map4(&tk, &a.wk, k, g.k, g.hk, g.b, g.nk, g.d, kTile);
   if (e == cudaSuccess) e = make_map4(&tv, &a.wv, v, g.v, g.hk, g.b, g.nk, g.d, kTile);
+  if (e == cudaSuccess) e = make_map4(&to, &whole, o, g.o, g.h, g.b, g.nq, g.d, kTile);
   if (e != cudaSuccess) return e;
   a.g = g;
   a.keys = keys;
@@ -578,13 +610,18 @@ cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const vo
   a.slices = p.slices;
   a.pairs = p.pairs;
   a.items = (int)p.items;
+  a.by_ks = divisor(p.ks);
+  a.by_pairs = divisor(p.pairs);
+  a.by_heads = divisor(p.packed ? g.hk : g.h);
+  a.by_group = divisor(g.group);
+  a.by_nq = divisor(g.nq);
   a.o = o;
   a.lse = lse;
   a.part = carve_fwd(g, p.ks, work);
   a.err = device_error_word();
   const int sms = sm_count();
   const int grid = a.items < sms ? a.items : sms;
-  e = g.d <= 64 ? launch<1>(a, tq, tk, tv, grid, s) : launch<2>(a, tq, tk, tv, grid, s);
+  e = g.d <= 64 ? launch<1>(a, tq, tk, tv, to, grid, s) : launch<2>(a, tq, tk, tv, to, grid, s);
   if (e == cudaSuccess && p.ks > 1) e = launch_join_fwd(g, p.ks, a.part, o, lse, s);
   return e;
 }

@@ -250,30 +250,63 @@ __global__ void join_fwd_kernel(const __grid_constant__ Geo g, int ks, FwdWork p
 
 // ------------------------------------------------------------------ backward
 
-// D = rowsum(dO * O): eight threads per row, four channels at a time.
+// D = rowsum(dO * O).  Eight threads per row, 16 bytes of it each at a time;
+// two rows per thread group are on their way at once.
 template <typename T>
-__global__ void row_dot_kernel(const __grid_constant__ Geo g, const T* __restrict__ o, const T* __restrict__ dO,
-                               float* __restrict__ D) {
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      r = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), r);
+      r = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), r);
+    } else {
+      r = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), r);
+    }
+  }
+  return r;
+}
+template <typename T>
+__global__ void __launch_bounds__(256) row_dot_kernel(const __grid_constant__ Geo g, Divisor by_nq, Divisor by_h,
+                                                      const T* __restrict__ o, const T* __restrict__ dO,
+                                                      float* __restrict__ D) {
+  constexpr int V = 16 / sizeof(T), STEPS = 128 / (8 * V);     // d <= 128: 2 or 4 loads of 16 bytes a thread
   const int64_t rows = rows_of(g);
   const int sub = threadIdx.x & 7;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x / 8);
-  const int64_t first = (int64_t)blockIdx.x * (blockDim.x / 8) + (threadIdx.x >> 3);
-  for (int64_t r0 = first - (threadIdx.x >> 3) % 4; r0 < rows; r0 += step) {     // uniform over the warp
-    const int64_t r = r0 + (threadIdx.x >> 3) % 4;
-    float x = 0.f;
-    if (r < rows) {
-      const int64_t bh = r / g.nq;
-      const int64_t n = r % g.nq, b = bh / g.h, h = bh % g.h;
+  for (int64_t r0 = (int64_t)blockIdx.x * 64; r0 < rows; r0 += (int64_t)gridDim.x * 64) {
+    uint4 a[2][STEPS], e[2][STEPS];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = r0 + 32 * k + (threadIdx.x >> 3);
+      if (r >= rows) continue;
+      // rows are fewer than 2^34: batch row by the 64-bit quotient, the rest in 32 bits
+      const int64_t bh64 = rows <= 0xffffffffll ? (int64_t)over((uint32_t)r, by_nq) : r / g.nq;
+      const int64_t n = r - bh64 * g.nq;
+      const uint32_t b = over((uint32_t)bh64, by_h);
+      const int64_t h = bh64 - (int64_t)b * g.h;
       const T* po = o + b * g.o.b + h * g.o.h + n * g.o.n;
       const T* pg = dO + b * g.dO.b + h * g.dO.h + n * g.dO.n;
-      for (int c = sub * 4; c < g.d; c += 32) {
-        const float4 a = load4(po + c), e = load4(pg + c);
-        x = fmaf(a.x, e.x, fmaf(a.y, e.y, fmaf(a.z, e.z, fmaf(a.w, e.w, x))));
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int c = (8 * i + sub) * V;
+        if (c < g.d) {
+          a[k][i] = *reinterpret_cast<const uint4*>(po + c);
+          e[k][i] = *reinterpret_cast<const uint4*>(pg + c);
+        }
       }
     }
 #pragma unroll
-    for (int w = 4; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    if (r < rows && sub == 0) D[r] = x;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = r0 + 32 * k + (threadIdx.x >> 3);
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        if (r < rows && (8 * i + sub) * V < g.d) x += dot16<T>(a[k][i], e[k][i]);
+#pragma unroll
+      for (int w = 4; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+      if (r < rows && sub == 0) D[r] = x;
+    }
   }
 }
 
@@ -548,11 +581,12 @@ cudaError_t launch_join_fwd(const Geo& g, int ks, const FwdWork& w, void* o, flo
 }
 
 cudaError_t launch_row_dot(const Geo& g, const void* o, const void* dO, float* D, cudaStream_t s) {
-  const int grid = grid_for(rows_of(g), 32);
+  const int grid = grid_for(rows_of(g), 64);
+  const Divisor n = divisor(g.nq), h = divisor(g.h);
   if (g.bf16)
-    row_dot_kernel<<<grid, 256, 0, s>>>(g, (const __nv_bfloat16*)o, (const __nv_bfloat16*)dO, D);
+    row_dot_kernel<<<grid, 256, 0, s>>>(g, n, h, (const __nv_bfloat16*)o, (const __nv_bfloat16*)dO, D);
   else
-    row_dot_kernel<<<grid, 256, 0, s>>>(g, (const float*)o, (const float*)dO, D);
+    row_dot_kernel<<<grid, 256, 0, s>>>(g, n, h, (const float*)o, (const float*)dO, D);
   note_launches(1);
   return cudaGetLastError();
 }

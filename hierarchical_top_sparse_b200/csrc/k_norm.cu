@@ -19,6 +19,7 @@
 // partial row, and a second kernel adds the partial rows: no atomics, the same
 // bits every time.
 #include "norm.cuh"
+#include "packed.cuh"
 
 namespace llsa {
 namespace norm {
@@ -114,36 +115,6 @@ __device__ __forceinline__ int64_t offset(const At& a, const int64_t* st, int gr
   return a.i0 * st[0] + a.i1 * st[1] + a.i2 * st[2] + group * st[3];
 }
 
-// Two fp32 values in one register pair, and the instructions that take both at
-// once: a norm's arithmetic per byte is enough to fill the issue slots.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pair(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ f2 twice(float a) { return pair(a, a); }
-__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ float both(f2 v) {
-  float a, b;
-  split(v, a, b);
-  return a + b;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // V values as pairs (of one value: its other half is zero).
 template <int V> constexpr int pairs() { return (V + 1) / 2; }
 template <typename T, int V>

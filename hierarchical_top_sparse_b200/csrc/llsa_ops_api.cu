@@ -162,8 +162,8 @@ static llsa_status make_norm(const llsa_norm_problem* p, norm::Geo* g) {
   g->flat_bwd = flat[0] && flat[2] && flat[3];
   g->groups = p->per_batch ? p->batch : 1;
   g->rows = ln[0] * ln[1] * ln[2];
-  g->n2 = norm::divisor((uint32_t)ln[0]);
-  g->n1 = norm::divisor((uint32_t)ln[1]);
+  g->n2 = divisor((uint32_t)ln[0]);
+  g->n1 = divisor((uint32_t)ln[1]);
   for (int t = 0; t < 5; ++t) {
     for (int i = 0; i < 3; ++i) out[t][2 - i] = ls[t][i];
     out[t][3] = st[t][0];
