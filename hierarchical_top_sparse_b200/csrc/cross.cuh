@@ -83,6 +83,12 @@ TcPlan plan_fwd_tc(const Geo& g, int sms);
 cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
                           const Keys& keys, void* o, float* lse, void* work, cudaStream_t s);
 
+// Forward for at most 16 query rows a key head (bf16).
+bool token_supported(const Geo& g);
+size_t token_work_bytes(const Geo& g, int sms);
+cudaError_t launch_fwd_token(const Geo& g, int sms, const void* q, const void* k, const void* v, const Keys& keys,
+                             void* o, float* lse, void* work, cudaStream_t s);
+
 // Tensor-core backward (bf16).
 bool bwd_tc_supported(const Geo& g);
 size_t bwd_work_bytes_tc(const Geo& g, int sms);

@@ -219,7 +219,9 @@ llsa_status llsa_cross_query_sizes(const llsa_cross_problem* p, llsa_cross_buffe
   out->fwd_workspace_bytes = llsa::cross::fwd_work_bytes(g, plan.fwd_ks);
   out->bwd_workspace_bytes = llsa::cross::bwd_work_bytes_simt(g, plan);
   if (g.bf16) {                                 // the strides decide which kernels run: room for either
-    const size_t tc = llsa::cross::fwd_work_bytes(g, llsa::cross::plan_fwd_tc(g, llsa::kSms).ks);
+    const size_t tc = llsa::cross::token_supported(g)
+                          ? llsa::cross::token_work_bytes(g, llsa::kSms)
+                          : llsa::cross::fwd_work_bytes(g, llsa::cross::plan_fwd_tc(g, llsa::kSms).ks);
     if (tc > out->fwd_workspace_bytes) out->fwd_workspace_bytes = tc;
     const size_t bwd = llsa::cross::bwd_work_bytes_tc(g, llsa::kSms);
     if (bwd > out->bwd_workspace_bytes) out->bwd_workspace_bytes = bwd;
@@ -238,6 +240,10 @@ llsa_status llsa_cross_attn_fwd(const llsa_cross_problem* p, const void* q, cons
   LLSA_MAY(kv_len, 4);
   LLSA_MAY(lse, 16);
   const llsa::cross::Keys keys{kv_len, key_mask};
+  if (llsa::cross::token_supported(g)) {
+    LLSA_NEED(workspace);
+    return llsa::launched(llsa::cross::launch_fwd_token(g, llsa::kSms, q, k, v, keys, o, lse, workspace, (cudaStream_t)stream));
+  }
   if (llsa::cross::fwd_tc_supported(g)) {
     const llsa::cross::TcPlan plan = llsa::cross::plan_fwd_tc(g, llsa::kSms);
     if (plan.ks > 1) LLSA_NEED(workspace);
@@ -274,7 +280,7 @@ llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, cons
 
 llsa_status llsa_cross_attn_paths(const llsa_cross_problem* p, int* fwd_tc, int* bwd_tc) {
   LLSA_CROSS(p, g);
-  if (fwd_tc) *fwd_tc = llsa::cross::fwd_tc_supported(g);
+  if (fwd_tc) *fwd_tc = llsa::cross::token_supported(g) || llsa::cross::fwd_tc_supported(g);
   if (bwd_tc) *bwd_tc = llsa::cross::bwd_tc_supported(g);
   return LLSA_OK;
 }

@@ -383,14 +383,14 @@ _NO_STRIDES = (0, 0, 0)
 
 
 def _checked(name: str, x, shape, dt, device):
-    """The address of x, a CUDA tensor of this shape and type whose last dimension is contiguous."""
+    """The address of x, a tensor of this shape and type on this device."""
+    if x.shape == shape and x.dtype is dt and x.device == device:
+        return x.data_ptr()
     if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
     if x.dtype != dt:
         raise ValueError(f"{name}: {x.dtype}, expected {dt}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, expected {device}")
-    return x.data_ptr()
+    raise ValueError(f"{name}: on {x.device}, expected {device}")
 
 
 def _strides(name: str, x):
@@ -416,7 +416,7 @@ def _flat(name: str, x, shape, dt, device):
 def _work(x, nbytes: int, device):
     if x is None or isinstance(x, int):
         return x
-    if x.device != device or x.numel() * x.element_size() < nbytes or not x.is_contiguous():
+    if x.device != device or x.nbytes < nbytes or not x.is_contiguous():
         raise ValueError(f"workspace: expected {nbytes} contiguous bytes on {device}")
     return x.data_ptr()
 
@@ -428,17 +428,19 @@ def _torch_dtype(dtype: int):
 
 def _run(fn, what: str, device, stream, *args):
     """The call on the tensors' device, and on the given stream, else on the device's current one."""
-    from torch import cuda
+    from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: these calls take CUDA tensors")
     if stream is None:
-        stream = cuda.current_stream(device).cuda_stream
+        stream = _cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    before = cuda.current_device()
-    if before == device.index:
+    before = _cuda_getDevice()
+    if before == index:
         st = fn(*args, stream)
     else:
+        from torch import cuda
         cuda.set_device(device)
         try:
             st = fn(*args, stream)
