@@ -323,9 +323,15 @@ def offs_views(p: Problem, buf):
 
 
 class Pipeline:
-    """Device buffers of one problem, allocated once, and the path run through the C ABI."""
+    """Device buffers of one problem, allocated once, and the path run through the C ABI.
 
-    def __init__(self, p: Problem, device="cuda", backward: bool = True):
+    With qk_norm, q and k go through a layer norm over each head's channels first (``norm_q`` and ``norm_k``, eps
+    `norm_eps`), with the fp32 weights and biases [d] in ``q_weight``, ``q_bias``, ``k_weight``, ``k_bias`` (ones and
+    zeros at first).  Then q and k may have any batch, head and token strides; dq and dk are gradients of what was
+    passed in, and norm_q.dweight, norm_q.dbias, norm_k.dweight and norm_k.dbias those of the weights."""
+
+    def __init__(self, p: Problem, device="cuda", backward: bool = True, qk_norm: bool = False,
+                 norm_eps: float = 1e-6):
         import torch
         self.p = p
         _check(validate(p), "validate")
@@ -350,9 +356,19 @@ class Pipeline:
             self.dq = torch.empty(shape, dtype=dt, device=device)
             self.dk = torch.empty(shape, dtype=dt, device=device)
             self.dv = torch.empty(shape, dtype=dt, device=device)
+        self.qk_norm = qk_norm
+        if qk_norm:
+            n = NormProblem(p.batch, p.heads, p.N, p.d, eps=norm_eps, dtype=p.dtype, param_dtype=FP32)
+            self.norm_q, self.norm_k = (LayerNorm(n, device, backward, own_dx=False) for _ in range(2))
+            self.q_weight, self.k_weight = (torch.ones(p.d, dtype=f32, device=device) for _ in range(2))
+            self.q_bias, self.k_bias = (torch.zeros(p.d, dtype=f32, device=device) for _ in range(2))
 
     def forward(self, q, k, v, stream=None):
         p = self.p
+        if self.qk_norm:
+            stream = _stream(stream)
+            q = self.norm_q.forward(q, self.q_weight, self.q_bias, stream)
+            k = self.norm_k.forward(k, self.k_weight, self.k_bias, stream)
         pool(p, q, self.pyrQ, stream)
         pool(p, k, self.pyrK, stream)
         pool(p, v, self.pyrV, stream)
@@ -362,9 +378,16 @@ class Pipeline:
 
     def backward_pass(self, q, k, v, dO, stream=None):
         p = self.p
+        x, y = q, k
+        if self.qk_norm:                                    # the attention saw the normed q and k of the forward call
+            stream = _stream(stream)
+            q, k = self.norm_q.y, self.norm_k.y
         index_transpose(p, self.idx, self.offs, self.qlist, self.tscratch, stream)
         attn_bwd(p, q, k, v, self.o, dO, self.lse, self.pyrK, self.pyrV, self.idx, self.offs, self.qlist,
                  self.dq, self.dk, self.dv, self.work, stream)
+        if self.qk_norm:                                    # in place: from the normed to what was passed in
+            self.norm_q.backward_pass(x, self.q_weight, self.dq, stream, dx=self.dq)
+            self.norm_k.backward_pass(y, self.k_weight, self.dk, stream, dx=self.dk)
         return self.dq, self.dk, self.dv
 
     def step(self, q, k, v, dO=None, stream=None):
@@ -703,9 +726,11 @@ def layer_norm_bwd(p: NormProblem, x, dy, weight, mean, rstd, dx=None, dweight=N
 
 
 class LayerNorm:
-    """Buffers of one layer-norm problem, allocated once, and its passes (token_major as for CrossAttention)."""
+    """Buffers of one layer-norm problem, allocated once, and its passes (token_major as for CrossAttention).  Without
+    own_dx the backward pass writes dx where it is told to (dx=)."""
 
-    def __init__(self, p: NormProblem, device="cuda", backward: bool = True, token_major: bool = False):
+    def __init__(self, p: NormProblem, device="cuda", backward: bool = True, token_major: bool = False,
+                 own_dx: bool = True):
         import torch
         self.p = p
         _check(norm_validate(p), "norm_validate")
@@ -716,7 +741,7 @@ class LayerNorm:
         if backward:
             self.mean = torch.empty(p.shape[:3], dtype=torch.float32, device=device)
             self.rstd = torch.empty(p.shape[:3], dtype=torch.float32, device=device)
-            self.dx = _buffer(p.shape, dt, device, token_major)
+            self.dx = _buffer(p.shape, dt, device, token_major) if own_dx else None
             self.dweight = torch.empty(p.param_shape, dtype=pt, device=device)
             self.dbias = torch.empty(p.param_shape, dtype=pt, device=device)
             self.work = torch.empty(norm_query_sizes(p)["bwd_workspace_bytes"], dtype=torch.uint8, device=device)
@@ -725,8 +750,9 @@ class LayerNorm:
         layer_norm_fwd(self.p, x, weight, bias, self.y, self.mean, self.rstd, stream)
         return self.y
 
-    def backward_pass(self, x, weight, dy, stream=None):
-        """The gradients of the last forward call (its mean and rstd are read)."""
-        layer_norm_bwd(self.p, x, dy, weight, self.mean, self.rstd, self.dx, self.dweight, self.dbias, self.work,
-                       stream)
-        return self.dx, self.dweight, self.dbias
+    def backward_pass(self, x, weight, dy, stream=None, dx=None):
+        """The gradients of the last forward call (its mean and rstd are read); dx: where to, if not to self.dx (dy
+        itself will do)."""
+        dx = self.dx if dx is None else dx
+        layer_norm_bwd(self.p, x, dy, weight, self.mean, self.rstd, dx, self.dweight, self.dbias, self.work, stream)
+        return dx, self.dweight, self.dbias
