@@ -18,8 +18,9 @@
 // Items that split a key tile's queries leave fp32 partial sums, added in
 // order by a second kernel: no atomics.
 //
-// Warps: 0-7 softmax, 8-11 epilogue, 12 producer (TMA), 13 MMA issue of S and
-// dV, 14 of dP and dK, 15 lse and D; also gathers Q and dO where heads are packed.
+// Warps: 0-7 softmax, 8-11 epilogue, 12 producer of Q and dO (TMA), 13 MMA issue
+// of S and dV, 14 of dP and dK, 15 K and V, lse and D; also gathers Q and dO
+// where heads are packed.
 #include <math.h>
 
 #include "cross_tc.cuh"
@@ -274,7 +275,7 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       }
     }
   } else if (warp == PRODUCER) {
-    // ============================================================ producer
+    // ============================================================ producer of Q and dO
     if (lane == 0) {
       auto wait1 = [&](uint64_t* bar, uint32_t parity, int code) {
         if (ok && !ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
@@ -283,18 +284,9 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         }
         return ok;
       };
-      uint32_t tc_ = 0, ic = 0;
+      uint32_t tc_ = 0;
       for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
         const Item x = item_of(a, it);
-        if (x.n == 0) continue;
-        if (!wait1(&s.kvempty, (ic & 1) ^ 1, 144)) break;
-        ++ic;
-        ptx::mbar_arrive_expect_tx(&s.kvfull, 2 * kBytes);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          tma_load_4d(s.k + p * kPanel, &tk, 64 * p, x.key0, x.hk * a.wk.h, x.b * a.wk.b, &s.kvfull);
-          tma_load_4d(s.v + p * kPanel, &tv, 64 * p, x.key0, x.hk * a.wv.h, x.b * a.wv.b, &s.kvfull);
-        }
         for (int i = 0; i < x.n && !a.packed; ++i) {
           const uint32_t st = tc_ % ST;
           if (!wait1(&s.empty[st], ((tc_ / ST) & 1) ^ 1, 144)) break;
@@ -312,17 +304,28 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       }
       // After a timeout, do not leave while copies issued here may still be landing.
       if (!ok) {
-        if (ic) ptx::mbar_wait_bounded(&s.kvfull, (ic - 1) & 1, kWaitLimitNs);
         for (uint32_t c = tc_ > ST ? tc_ - ST : 0; c < tc_; ++c)
           ptx::mbar_wait_bounded(&s.full[c % ST], (c / ST) & 1, kWaitLimitNs);
       }
     }
     __syncwarp();
   } else if (warp == STATS) {
-    // ============================================================ lse and D; packed rows of Q and dO
-    uint32_t tc_ = 0;
+    // ============================================================ K and V; lse and D; packed rows of Q and dO
+    uint32_t tc_ = 0, ic = 0;
     for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item x = item_of(a, it);
+      if (x.n == 0) continue;
+      if (!wait(&s.kvempty, (ic & 1) ^ 1, 144)) break;
+      ++ic;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&s.kvfull, 2 * kBytes);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          tma_load_4d(s.k + p * kPanel, &tk, 64 * p, x.key0, x.hk * a.wk.h, x.b * a.wk.b, &s.kvfull);
+          tma_load_4d(s.v + p * kPanel, &tv, 64 * p, x.key0, x.hk * a.wv.h, x.b * a.wv.b, &s.kvfull);
+        }
+      }
+      __syncwarp();
       for (int i = 0; i < x.n; ++i, ++tc_) {
         const uint32_t st = tc_ % ST, si = tc_ % NSTAT;
         auto at = [&](int r, int& h, int& n) { return row_of(a, x.hk, x.u0 + i, r, h, n); };
@@ -352,6 +355,8 @@ bwd_kv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         }
       }
     }
+    if (!ok && lane == 0 && ic) ptx::mbar_wait_bounded(&s.kvfull, (ic - 1) & 1, kWaitLimitNs);   // (as above)
+    __syncwarp();
   } else {
     // ============================================================ MMA issue: r = 0: S^T and dV, r = 1: dP^T and dK
     const int r = warp - MMA0;

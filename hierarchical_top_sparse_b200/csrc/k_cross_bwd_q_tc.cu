@@ -10,8 +10,10 @@
 // while the next exponentials do.  Bound by the tensor cores from 128 channels
 // on, by the exponentials below.
 //
-// Warps: 0-7 softmax, 8-11 epilogue, 12 producer (TMA), 13 MMA issue, 14
-// clears masked rows of K and V, and gathers Q and dO where heads are packed.
+// Warps: 0-7 softmax, 8-11 epilogue, 12 producer of K and V (TMA), 13 MMA
+// issue, 14 fetches Q and dO (where heads are packed by plain loads) and clears
+// masked rows of K and V.  (One producer for all would hold the next item's
+// keys back until this one's queries are done with.)
 #include <math.h>
 
 #include "cross_tc.cuh"
@@ -246,7 +248,7 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
       }
     }
   } else if (warp == PRODUCER) {
-    // ============================================================ producer
+    // ============================================================ producer of K and V
     if (lane == 0) {
       auto wait1 = [&](uint64_t* bar, uint32_t parity, int code) {
         if (ok && !ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
@@ -255,21 +257,10 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         }
         return ok;
       };
-      uint32_t qc = 0, kc = 0, vc = 0;
+      uint32_t kc = 0, vc = 0;
       for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
         const Item x = item_of(a, it);
         if (x.n == 0) continue;
-        if (!a.packed) {
-          const uint32_t st = qc % QST;
-          if (!wait1(&s.qempty[st], ((qc / QST) & 1) ^ 1, 124)) break;
-          ++qc;
-          ptx::mbar_arrive_expect_tx(&s.qfull[st], 2 * kBytes);
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            tma_load_4d(s.q[st] + p * kPanel, &tq, 64 * p, x.row0, x.h * a.wq.h, x.b * a.wq.b, &s.qfull[st]);
-            tma_load_4d(s.dO[st] + p * kPanel, &tg, 64 * p, x.row0, x.h * a.wg.h, x.b * a.wg.b, &s.qfull[st]);
-          }
-        }
         for (int j = 0; j < x.n; ++j) {
           const int n0 = x.key0 + j * kTile;
           const uint32_t ki = kc % NK, vi = vc % NV;
@@ -289,8 +280,6 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
       }
       // After a timeout, do not leave while copies issued here may still be landing.
       if (!ok) {
-        for (uint32_t c = qc > QST ? qc - QST : 0; c < qc; ++c)
-          ptx::mbar_wait_bounded(&s.qfull[c % QST], (c / QST) & 1, kWaitLimitNs);
         for (uint32_t c = kc > NK ? kc - NK : 0; c < kc; ++c)
           ptx::mbar_wait_bounded(&s.kfull[c % NK], (c / NK) & 1, kWaitLimitNs);
         for (uint32_t c = vc > NV ? vc - NV : 0; c < vc; ++c)
@@ -299,22 +288,30 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     }
     __syncwarp();
   } else if (warp == FIXER) {
-    // ============================================================ rows of K and V; packed rows of Q and dO
+    // ============================================================ Q and dO; rows of K and V
     uint32_t kc = 0, qc = 0;
     for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item x = item_of(a, it);
       if (x.n == 0) continue;
+      const uint32_t st = qc % QST;
+      if (!wait(&s.qempty[st], ((qc / QST) & 1) ^ 1, 126)) break;
+      ++qc;
       if (a.packed) {
-        const uint32_t st = qc % QST;
-        if (!wait(&s.qempty[st], ((qc / QST) & 1) ^ 1, 126)) break;
-        ++qc;
-        gather_rows<NP>(s.q[st], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane,
-                        [&](int r, int& h, int& n) { return row_of(a, x, r, h, n); });
-        gather_rows<NP>(s.dO[st], static_cast<const __nv_bfloat16*>(a.dO) + x.b * g.dO.b, g.dO, g.d, lane,
-                        [&](int r, int& h, int& n) { return row_of(a, x, r, h, n); });
+        auto at = [&](int r, int& h, int& n) { return row_of(a, x, r, h, n); };
+        gather_rows<NP>(s.q[st], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane, at);
+        gather_rows<NP>(s.dO[st], static_cast<const __nv_bfloat16*>(a.dO) + x.b * g.dO.b, g.dO, g.d, lane, at);
         ptx::fence_proxy_async();
         arrive(&s.qfull[st]);
+      } else if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&s.qfull[st], 2 * kBytes);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          tma_load_4d(s.q[st] + p * kPanel, &tq, 64 * p, x.row0, x.h * a.wq.h, x.b * a.wq.b, &s.qfull[st]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          tma_load_4d(s.dO[st] + p * kPanel, &tg, 64 * p, x.row0, x.h * a.wg.h, x.b * a.wg.b, &s.qfull[st]);
       }
+      __syncwarp();
       const uint8_t* mask = a.keys.mask ? a.keys.mask + (int64_t)x.b * g.nk : nullptr;
       for (int j = 0; j < x.n; ++j, ++kc) {
         const int key0 = x.key0 + j * kTile;
@@ -336,6 +333,10 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         arrive(&s.vready[vi]);
       }
     }
+    if (!ok && lane == 0 && !a.packed)         // (as above)
+      for (uint32_t c = qc > QST ? qc - QST : 0; c < qc; ++c)
+        ptx::mbar_wait_bounded(&s.qfull[c % QST], (c / QST) & 1, kWaitLimitNs);
+    __syncwarp();
   } else if (warp == MMA) {
     // ============================================================ MMA issue
     const uint64_t qd = tc::sw128_desc(ptx::smem_u32(s.q[0]), 16, 1024);

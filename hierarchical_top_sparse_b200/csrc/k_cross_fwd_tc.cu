@@ -23,8 +23,10 @@
 // cleared in shared memory, so that 0 * V is 0 whatever V holds.
 //
 // Warps (one CTA per SM, items dealt round robin): 0-3 and 4-7 softmax of tile
-// 0 and 1, 8-11 epilogue, 12 producer (TMA), 13 MMA issue of S, 14 of O, 15
-// clears rows of V, and gathers Q where heads are packed.
+// 0 and 1, 8-11 epilogue, 12 producer of K and V (TMA), 13 MMA issue of S,
+// 14 of O, 15 fetches Q (where heads are packed by plain loads) and clears rows
+// of V.  (One producer for all would hold the next item's keys back until this
+// one's queries are done with.)
 // Up to 64 channels, P has columns of its own and S of the next key tile is
 // computed while P of this one is made; above, P takes S's columns.
 #include <math.h>
@@ -364,8 +366,8 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
       if (warp == EPI0 && lane == 0) tma_stores_done();
       __syncwarp();
     } else if (warp == PRODUCER) {
-      // ============================================================ producer
-      uint32_t qc[2] = {0, 0}, kc = 0;
+      // ============================================================ producer of K and V
+      uint32_t kc = 0;
       bool k_alone = false;                    // a K was asked for, its V not yet
       if (lane == 0) {
         auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
@@ -378,18 +380,6 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
           const Item x = item_of(a, it);
           if (x.n == 0) continue;
-#pragma unroll 1
-          for (int t = 0; t < a.tpi && !a.packed; ++t) {
-            const uint32_t c = qc[t];
-            uint64_t* full = &s.qfull[t][c % QST];
-            if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 95)) break;
-            ptx::mbar_arrive_expect_tx(full, kBytes);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-              tma_load_4d(s.q[t][c % QST] + p * kPanel, &tq, 64 * p, x.row0 + t * kTile, x.h * a.wq.h, x.b * a.wq.b,
-                          full);
-            ++qc[t];
-          }
           for (int j = 0; j < x.n && ok; ++j) {
             const uint32_t i = kc % NS, ph = ((kc / NS) & 1) ^ 1;
             if (!wait(&s.kempty[i], ph, 96)) break;
@@ -411,9 +401,6 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
         }
         // After a timeout, do not leave while copies issued here may still be landing.
         if (!ok) {
-          for (int t = 0; t < 2 && !a.packed; ++t)
-            for (uint32_t c = qc[t] > QST ? qc[t] - QST : 0; c < qc[t]; ++c)
-              lane_wait(&s.qfull[t][c % QST], (c / QST) & 1);
           for (uint32_t c = kc > NS ? kc - NS : 0; c < kc; ++c) {
             lane_wait(&s.kfull[c % NS], (c / NS) & 1);
             lane_wait(&s.vfull[c % NS], (c / NS) & 1);
@@ -423,17 +410,17 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
       }
       __syncwarp();
     } else if (warp == FIXER) {
-      // ============================================================ rows of V; packed queries
-      uint32_t kc = 0, qc[2] = {0, 0};
+      // ============================================================ Q; rows of V
+      uint32_t kc = 0, qc = 0;
       for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
         const Item x = item_of(a, it);
         if (x.n == 0) continue;
-        if (a.packed) {
 #pragma unroll 1
-          for (int t = 0; t < a.tpi; ++t) {
-            const uint32_t c = qc[t]++;
-            if (!wait(&s.qempty[t][c % QST], ((c / QST) & 1) ^ 1, 97)) break;
-            gather_rows<NP>(s.q[t][c % QST], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane,
+        for (int t = 0; t < a.tpi; ++t) {
+          uint64_t* full = &s.qfull[t][qc % QST];
+          if (!wait(&s.qempty[t][qc % QST], ((qc / QST) & 1) ^ 1, 97)) break;
+          if (a.packed) {
+            gather_rows<NP>(s.q[t][qc % QST], static_cast<const __nv_bfloat16*>(a.q) + x.b * g.q.b, g.q, g.d, lane,
                             [&](int r, int& h, int& n) {
                               const int rr = x.row0 + t * kTile + r;
                               h = x.h + divide(rr, a.by_nq, n);
@@ -441,10 +428,18 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
                             });
             ptx::fence_proxy_async();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.qfull[t][c % QST]);
+            if (lane == 0) ptx::mbar_arrive(full);
+          } else if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(full, kBytes);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              tma_load_4d(s.q[t][qc % QST] + p * kPanel, &tq, 64 * p, x.row0 + t * kTile, x.h * a.wq.h, x.b * a.wq.b,
+                          full);
           }
-          if (!ok) break;
+          __syncwarp();
         }
+        if (!ok) break;
+        ++qc;
         const uint8_t* mask = a.keys.mask ? a.keys.mask + (int64_t)x.b * g.nk : nullptr;
         for (int j = 0; j < x.n; ++j, ++kc) {
           const int key0 = x.key0 + j * kTile;
@@ -461,6 +456,10 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           if (lane == 0) ptx::mbar_arrive(&s.vready[i]);
         }
       }
+      if (!ok && lane == 0 && !a.packed)       // (as above; the last item's copies may not all have been asked for)
+        for (int t = 0; t < a.tpi; ++t)
+          for (uint32_t c = qc >= QST ? qc + 1 - QST : 0; c <= qc; ++c) lane_wait(&s.qfull[t][c % QST], (c / QST) & 1);
+      __syncwarp();
     } else {
       // ============================================================ MMA issue: one warp S, one O
       const bool is_s = warp == MMA_S;
