@@ -131,27 +131,20 @@ __device__ __forceinline__ uint64_t half_bits(const uint8_t* mask, int key0, int
 }
 
 // Zeros the rows of a swizzled [128][64 x panels] tile whose bit is clear
-// (every lane of one warp).
+// (every lane of one warp): four rows at a time, eight lanes a row.
 template <int PANELS>
 __device__ __forceinline__ void clear_rows(unsigned char* tile, const uint32_t bits[4], int lane) {
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    uint32_t off = ~bits[i];
-    while (off) {
-      // four rows at a time: eight lanes write a row's eight 16-byte chunks
-      int row = -1;
+  unsigned char* at = tile + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int first = off ? __ffs(off) - 1 : -1;
-        if (lane >> 3 == k) row = first;
-        off &= off - 1;
-      }
-      if (row >= 0)
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t off = ~bits[i] >> (lane >> 3);
+    if (bits[i] == 0xffffffffu) continue;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if ((off >> (4 * r)) & 1u)
 #pragma unroll
         for (int p = 0; p < PANELS; ++p)
-          *reinterpret_cast<uint4*>(tile + p * kPanel + (32 * i + row) * 128 + (lane & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-    }
+          *reinterpret_cast<uint4*>(at + p * kPanel + (32 * i + 4 * r) * 128) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
