@@ -120,16 +120,6 @@ __device__ __forceinline__ void key_bits(const uint8_t* mask, int key0, int n, i
   }
 }
 
-// The bits of a half of the keys: 16 * units from column col0 (16 * units or 0) on.
-__device__ __forceinline__ uint64_t half_bits(const uint8_t* mask, int key0, int n, int lane, uint32_t col0,
-                                              int units) {
-  uint32_t w[4];
-  key_bits(mask, key0, n, lane, w);
-  const uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
-  const uint64_t bits = col0 == 0 ? lo : (col0 == 64 ? hi : (lo >> col0) | (hi << (64 - col0)));
-  return units >= 4 ? bits : bits & ((1ull << (16 * units)) - 1);
-}
-
 // Zeros the rows of a swizzled [128][64 x panels] tile whose bit is clear
 // (every lane of one warp): four rows at a time, eight lanes a row.
 template <int PANELS>

@@ -49,19 +49,26 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
 template <typename T, int DP, int ROWS>
 __device__ __forceinline__ void load_tile(float* t, int ld, float* nrm, const T* base, int64_t stride, int row0, int n,
                                           int d, const uint8_t* mask) {
-  constexpr int C4 = DP / 4;
-  for (int i = threadIdx.x; i < ROWS * C4; i += THREADS) {
+  constexpr int C4 = DP / 4, N = ROWS * C4 / THREADS;
+  float4 x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {                          // all of a thread's loads first: one latency, not N
+    const int i = threadIdx.x + k * THREADS;
+    const int c = ((i >> 3) % C4) * 4, row = row0 + (i & 7) + 8 * ((i >> 3) / C4);
+    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < n && c < d && (!mask || mask[row])) x[k] = load4(base + (int64_t)row * stride + c);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = threadIdx.x + k * THREADS;
     const int c = ((i >> 3) % C4) * 4, r = (i & 7) + 8 * ((i >> 3) / C4);
-    const int row = row0 + r;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < n && c < d && (!mask || mask[row])) x = load4(base + (int64_t)row * stride + c);
     if (t) {
-      t[(c + 0) * ld + r] = x.x;
-      t[(c + 1) * ld + r] = x.y;
-      t[(c + 2) * ld + r] = x.z;
-      t[(c + 3) * ld + r] = x.w;
+      t[(c + 0) * ld + r] = x[k].x;
+      t[(c + 1) * ld + r] = x[k].y;
+      t[(c + 2) * ld + r] = x[k].z;
+      t[(c + 3) * ld + r] = x[k].w;
     }
-    if (nrm) store4(nrm + r * (DP + 4) + c, x);
+    if (nrm) store4(nrm + r * (DP + 4) + c, x[k]);
   }
 }
 
@@ -165,8 +172,9 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Ge
     for (int j = 0; j < 4; ++j)
       store4(s.pt + (tx * 4 + j) * LD + ty * 4, make_float4(z[0][j], z[1][j], z[2][j], z[3][j]));
     __syncthreads();
+    const int live = min(BN, n - key0);                  // the weights behind are zero
 #pragma unroll 4
-    for (int key = 0; key < BN; ++key) {
+    for (int key = 0; key < live; ++key) {
       const float4 p = *reinterpret_cast<const float4*>(s.pt + key * LD + ty * 4);
       const float ps[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -371,8 +379,9 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Geo
       store4(s.st + (tx * 4 + j) * LD + ty * 4, make_float4(x[0], x[1], x[2], x[3]));
     }
     __syncthreads();
+    const int live = min(BN, n - key0);
 #pragma unroll 4
-    for (int key = 0; key < BN; ++key) {
+    for (int key = 0; key < live; ++key) {
       const float4 p = *reinterpret_cast<const float4*>(s.st + key * LD + ty * 4);
       const float ps[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
