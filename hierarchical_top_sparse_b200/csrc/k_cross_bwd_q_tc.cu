@@ -3,11 +3,14 @@
 //
 // An item is one tile of 128 query rows against the key tiles of one split:
 //   S = Q K^T, dP = dO V^T              (M = 128 queries, N = the tile's keys)
-//   dS = 2^(z - lse) o (dP - D)         as bf16 into S's columns, each half into its own
+//   dS = 2^(z - lse) o (dP - D)         as two bf16 (the value and what rounding left) over S
 //   dQ += dS K                          (A = dS from TMEM, accumulated in TMEM)
 // Two threads share a row, each half of a tile's key columns.  S has two
 // buffers: the next tile's S is computed while this one's softmax runs, its dP
-// while the next exponentials do.  Bound by the tensor cores from 128 channels
+// while the next exponentials do.  D comes from the rounded O; with dS rounded
+// as well dQ was 2.6e-3 off (relative to its norm) where the result's own
+// rounding makes 1.7e-3; the second bf16 costs products that the tensor cores
+// have time for.  Bound by the tensor cores from 128 channels
 // on, by the exponentials below.
 //
 // Warps: 0-7 softmax, 8-11 epilogue, 12 producer of K and V (TMA), 13 MMA
@@ -195,14 +198,17 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (c < chunks) {
-            uint32_t r[16], w[8];
+            uint32_t r[16], w[16];               // 16 columns of S become 8 of dS and 8 of what the rounding left
             tc::tmem_ld16(tl + COL_DP + col0 + 16u * c, r);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] = ptx::pack_bf16(p[16 * c + 2 * e] * (__uint_as_float(r[2 * e]) - D),
-                                    p[16 * c + 2 * e + 1] * (__uint_as_float(r[2 * e + 1]) - D));
-            tc::tmem_st8(cs + col0 + 8u * c, w);
+            for (int e = 0; e < 8; ++e) {
+              const float x0 = p[16 * c + 2 * e] * (__uint_as_float(r[2 * e]) - D);
+              const float x1 = p[16 * c + 2 * e + 1] * (__uint_as_float(r[2 * e + 1]) - D);
+              w[e] = ptx::pack_bf16(x0, x1);
+              w[8 + e] = ptx::pack_bf16(x0 - __uint_as_float(w[e] << 16), x1 - __uint_as_float(w[e] & 0xffff0000u));
+            }
+            tc::tmem_st16(cs + col0 + 16u * c, w);
           }
         tc::fence_before_sync();
         arrive(&s.dp_free);
@@ -386,12 +392,14 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         if (!wait(&s.ds_full[sb], (c >> 1) & 1, 128)) return;
         if (j == 0 && !wait(&s.dq_free, (ic & 1) ^ 1, 128)) return;
         tc::fence_after_sync();
-        const int steps = tile_cols(x, j) >> 4, mid = steps >> 1;
+        const int steps = tile_cols(x, j) >> 4;
         const uint32_t ds = tbase + COL_S + 128u * sb;
         if (tc::elect_one()) {
-          for (int k = 0; k < steps; ++k)      // 16 keys: 8 columns of dS (the second half's start at its own S)
-            tc::mma_bf16_ta(tbase + COL_DQ, ds + (k < mid ? 8u * k : 16u * mid + 8u * (k - mid)),
-                            kd_mn + (c % NK) * kStep + 128u * k, id_q, j > 0 || k > 0);
+          for (int k = 0; k < steps; ++k)      // 16 keys: 8 columns of dS, then 8 of its rest
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              tc::mma_bf16_ta(tbase + COL_DQ, ds + 16u * k + 8u * e, kd_mn + (c % NK) * kStep + 128u * k, id_q,
+                              j > 0 || k > 0 || e > 0);
           tc::commit(&s.s_free[sb]);
           tc::commit(&s.kempty[c % NK]);
         }
