@@ -16,9 +16,6 @@ constexpr int kPanel = kTile * 128;  // bytes of a [128][64] bf16 panel, 128-byt
 // A token tensor as TMA sees it: channels, tokens, heads, batch rows.  A head
 // or batch dimension that the tensor repeats (stride 0), or of one, is left
 // out: its coordinate is always 0.
-struct Map4 {
-  CUtensorMap map;
-};
 struct Where {
   int h, b;                          // factors of the head and batch coordinates: 1, or 0 where left out
 };
@@ -171,61 +168,6 @@ __device__ __forceinline__ void store16(const float* f, __nv_bfloat16* out, floa
       d4[3] = make_float4(f[12], f[13], f[14], f[15]);
     }
   }
-}
-
-// Result rows on their way out: the four epilogue warps write a panel of 128
-// rows and 64 channels in shared memory and one thread sends it by TMA, which
-// clips rows and channels behind the ends.  (Each thread storing its own row
-// takes 32 lines an instruction, and everything else that uses the memory
-// pipe, mbarriers and tensor-memory loads among it, queues behind.)
-struct Outgoing {
-  alignas(1024) unsigned char tile[kPanel];
-  alignas(8) uint64_t full, free;
-};
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int n, int h, int b) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(n), "r"(h), "r"(b), "r"(ptx::smem_u32(src))
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// One panel: values(c, f) gives this thread's 16 values from column 16 c of the
-// panel on; `count` panels went before; wait(barrier, parity) as in the kernels.
-// False when a wait ran out.
-template <typename Values, typename Wait>
-__device__ __forceinline__ bool send_panel(Outgoing& o, uint32_t count, bool leader, int lane, int row,
-                                           const CUtensorMap* map, int x, int n, int h, int b, bool any, Values values,
-                                           Wait wait) {
-  if (count > 0) {
-    if (leader && lane == 0) {
-      tma_stores_read();
-      ptx::mbar_arrive(&o.free);
-    }
-    __syncwarp();
-    if (!wait(&o.free, (count - 1) & 1)) return false;
-  }
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    float f[16];
-    values(c, f);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      *reinterpret_cast<uint4*>(o.tile + row * 128 + (((2 * c + e) ^ (row & 7)) << 4)) =
-          make_uint4(ptx::pack_bf16(f[8 * e], f[8 * e + 1]), ptx::pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                     ptx::pack_bf16(f[8 * e + 4], f[8 * e + 5]), ptx::pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-  }
-  ptx::fence_proxy_async();
-  __syncwarp();
-  if (lane == 0) ptx::mbar_arrive(&o.full);
-  __syncwarp();
-  if (!leader) return true;
-  if (!wait(&o.full, count & 1)) return false;
-  if (lane == 0 && any) tma_store_4d(map, o.tile, x, n, h, b);
-  __syncwarp();
-  return true;
 }
 
 inline int sm_count() {

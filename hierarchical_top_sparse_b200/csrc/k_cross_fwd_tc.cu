@@ -71,7 +71,6 @@ struct Smem {
   alignas(1024) unsigned char q[2][QST][NP * kPanel];
   alignas(1024) unsigned char k[NS][NP * kPanel];
   alignas(1024) unsigned char v[NS][NP * kPanel];
-  Outgoing out;
   float stat_m[2][128], stat_l[2][128];        // an item's row maxima and sums: softmax -> epilogue
   alignas(8) uint64_t qfull[2][QST], qempty[2][QST];
   uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], vready[NS];
@@ -126,8 +125,7 @@ template <int NP>
 __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constant__ Args a,
                                                             const __grid_constant__ CUtensorMap tq,
                                                             const __grid_constant__ CUtensorMap tk,
-                                                            const __grid_constant__ CUtensorMap tv,
-                                                            const __grid_constant__ CUtensorMap to) {
+                                                            const __grid_constant__ CUtensorMap tv) {
   using S = Smem<NP>;
   constexpr int QST = S::QST, NS = S::NS;
   constexpr uint32_t kBytes = NP * kPanel;
@@ -157,8 +155,6 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
       ptx::mbar_init(&s.vempty[i], 1);
       ptx::mbar_init(&s.vready[i], 1);
     }
-    ptx::mbar_init(&s.out.full, 4);
-    ptx::mbar_init(&s.out.free, 1);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -303,8 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
       // ============================================================ epilogue
       const int sub = warp & 3;
       const uint32_t tl = tbase + ((uint32_t)(sub * 32) << 16);
-      uint32_t oc[2] = {0, 0}, sent = 0;
-      const bool direct = a.packed || a.ks > 1;    // rows that TMA cannot place, or fp32 parts
+      uint32_t oc[2] = {0, 0};
       for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
         const Item x = item_of(a, it);
 #pragma unroll 1
@@ -327,30 +322,16 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           const int64_t at = ((int64_t)x.b * g.h + h) * g.nq + n;
           __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.o) + x.b * g.o.b + h * g.o.h + n * g.o.n;
           float* pp = a.part.o + ((int64_t)x.split * rows_of(g) + at) * g.d;
-          auto values = [&](int col, float* f) {
+#pragma unroll 1
+          for (int c = 0; c < g.d; c += 16) {
             uint32_t w[16];
-            tc::tmem_ld16(tl + col_o(t) + col, w);
+            tc::tmem_ld16(tl + col_o(t) + c, w);
             tc::tmem_wait_ld();
+            float f[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] = none ? 0.f : __uint_as_float(w[e]) * inv;
-          };
-          if (direct) {
-#pragma unroll 1
-            for (int c = 0; c < g.d; c += 16) {
-              float f[16];
-              values(c, f);
-              if (live) store16(f, a.ks > 1 ? nullptr : po + c, pp + c, c + 8 < g.d);
-              __syncwarp();
-            }
-          } else {
-            const int n0 = x.row0 + t * kTile;
-#pragma unroll 1
-            for (int p = 0; p < NP; ++p, ++sent)
-              if (!send_panel(s.out, sent, warp == EPI0, lane, sub * 32 + lane, &to, 64 * p, n0, x.h, x.b, n0 < x.rows,
-                              [&](int c, float* f) { values(64 * p + 16 * c, f); },
-                              [&](uint64_t* bar, uint32_t parity) { return wait(bar, parity, 100); }))
-                break;
-            if (!ok) break;
+            if (live) store16(f, a.ks > 1 ? nullptr : po + c, pp + c, c + 8 < g.d);
+            __syncwarp();
           }
           if (live) {
             if (a.ks > 1)
@@ -363,8 +344,6 @@ __global__ void __launch_bounds__(THREADS, 1) fwd_tc_kernel(const __grid_constan
           if (lane == 0) ptx::mbar_arrive(&s.o_empty[t]);
         }
       }
-      if (warp == EPI0 && lane == 0) tma_stores_done();
-      __syncwarp();
     } else if (warp == PRODUCER) {
       // ============================================================ producer of K and V
       uint32_t kc = 0;
@@ -579,12 +558,12 @@ TcPlan plan_fwd_tc(const Geo& g, int sms) {
 
 template <int NP>
 static cudaError_t launch(const fwdtc::Args& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          const CUtensorMap& to, int grid, cudaStream_t s) {
+                          int grid, cudaStream_t s) {
   const size_t smem = sizeof(fwdtc::Smem<NP>) + 1024;
   cudaError_t e =
       cudaFuncSetAttribute(fwdtc::fwd_tc_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  fwdtc::fwd_tc_kernel<NP><<<grid, fwdtc::THREADS, smem, s>>>(a, tq, tk, tv, to);
+  fwdtc::fwd_tc_kernel<NP><<<grid, fwdtc::THREADS, smem, s>>>(a, tq, tk, tv);
   note_launches(1);
   return cudaGetLastError();
 }
@@ -592,12 +571,10 @@ static cudaError_t launch(const fwdtc::Args& a, const CUtensorMap& tq, const CUt
 cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const void* k, const void* v,
                           const Keys& keys, void* o, float* lse, void* work, cudaStream_t s) {
   fwdtc::Args a;
-  CUtensorMap tq, tk, tv, to;
-  Where whole;                                 // a result repeats nothing: its coordinates are all its own
+  CUtensorMap tq, tk, tv;
   cudaError_t e = make_map4(&tq, &a.wq, q, g.q, g.h, g.b, g.nq, g.d, kTile);
   if (e == cudaSuccess) e = make_map4(&tk, &a.wk, k, g.k, g.hk, g.b, g.nk, g.d, kTile);
   if (e == cudaSuccess) e = make_map4(&tv, &a.wv, v, g.v, g.hk, g.b, g.nk, g.d, kTile);
-  if (e == cudaSuccess) e = make_map4(&to, &whole, o, g.o, g.h, g.b, g.nq, g.d, kTile);
   if (e != cudaSuccess) return e;
   a.g = g;
   a.keys = keys;
@@ -620,7 +597,7 @@ cudaError_t launch_fwd_tc(const Geo& g, const TcPlan& p, const void* q, const vo
   a.err = device_error_word();
   const int sms = sm_count();
   const int grid = a.items < sms ? a.items : sms;
-  e = g.d <= 64 ? launch<1>(a, tq, tk, tv, to, grid, s) : launch<2>(a, tq, tk, tv, to, grid, s);
+  e = g.d <= 64 ? launch<1>(a, tq, tk, tv, grid, s) : launch<2>(a, tq, tk, tv, grid, s);
   if (e == cudaSuccess && p.ks > 1) e = launch_join_fwd(g, p.ks, a.part, o, lse, s);
   return e;
 }
