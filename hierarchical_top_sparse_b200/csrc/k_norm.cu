@@ -165,7 +165,9 @@ template <int G> constexpr int threads() { return G <= 32 ? 256 : G; }
 // Rows of a step and thread group.  Two where a thread holds one vector of each (with four the registers leave too few
 // blocks: 51 us against 44 for 786432 rows of 64 bf16 channels).
 template <int G, int IT, int V> constexpr int rows_at_once() {
-  return G > 32 || V == 1 || IT > 1 ? 1 : 2;
+  if (V > 1) return G > 32 || IT > 1 ? 1 : 2;
+  if (G > 32) return 1;
+  return IT <= 2 ? 4 : (IT <= 4 ? 2 : 1);
 }
 
 template <typename T, int V, int G, int IT>
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(threads<G>()) fwd_kernel(const __grid_constant
   constexpr int RPB = threads<G>() / G;              // thread groups of a block
   constexpr int R = rows_at_once<G, IT, V>();
   constexpr bool KEEP = G <= 32;                     // weights in registers; a block-wide row reads them again (from L1)
-  __shared__ float red[G > 32 ? 2 * 32 : 1];
+  __shared__ float red[G > 32 ? 2 * R * 32 : 1];
   int turn = 0;
   const int sub = threadIdx.x % G, slot = threadIdx.x / G;
   const int group = blockIdx.y;
@@ -309,9 +311,9 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
                                                            const float* __restrict__ rstd, T* dx,
                                                            float* __restrict__ part) {
   constexpr int RPB = threads<G>() / G;
-  constexpr int R = G > 32 || V == 1 || IT > 1 ? 1 : 2;
+  constexpr int R = V > 1 ? (G > 32 || IT > 1 ? 1 : 2) : (G > 32 ? (G == 128 ? 2 : 1) : (IT <= 2 ? 4 : (IT <= 4 ? 2 : 1)));
   constexpr int NV = IT * V;
-  __shared__ float red[G > 32 ? 2 * 2 * 32 : 1];
+  __shared__ float red[G > 32 ? 2 * 2 * R * 32 : 1];
   __shared__ float cols[G <= 32 ? 8 * G * NV : 1];   // a block's eight warps' sums
   int turn = 0;
   const int sub = threadIdx.x % G, slot = threadIdx.x / G;
@@ -551,11 +553,16 @@ static Shape shape_of(const Geo& g, bool bwd) {
     return {v, 1024, 4};
   }
   if (g.c <= 8) return {1, 8, 1};
-  if (g.c <= 32) return {1, 32, 1};
-  if (g.c <= 128) return {1, 32, 4};
+  if (g.c <= 16) return {1, 8, 2};
+  if (g.c <= 32) return {1, 8, 4};
+  if (g.c <= 64) return {1, 8, 8};
+  if (g.c <= 128) return {1, 16, 8};
   if (g.c <= 256) return {1, 32, 8};
+  if (g.c <= 512) return {1, 128, 4};
   if (g.c <= 1024) return bwd ? Shape{1, 256, 4} : Shape{1, 128, 8};
+  if (g.c <= 2048) return {1, 512, 4};
   if (g.c <= 4096) return {1, 512, 8};
+  if (g.c <= 8192) return bwd ? Shape{1, 512, 16} : Shape{1, 1024, 8};
   return {1, 1024, 16};
 }
 
@@ -576,7 +583,8 @@ int bwd_parts(const Geo& g) {
 #define NORM_FWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 32, 3) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 256, 2)
 #define NORM_BWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 128, 1) F(T, V, 256, 1) F(T, V, 512, 1)
 #define NORM_ONE_SHAPES(F, T) \
-  F(T, 1, 8, 1) F(T, 1, 32, 1) F(T, 1, 32, 4) F(T, 1, 32, 8) F(T, 1, 512, 8) F(T, 1, 1024, 16)
+  F(T, 1, 8, 1) F(T, 1, 8, 2) F(T, 1, 8, 4) F(T, 1, 8, 8) F(T, 1, 16, 8) F(T, 1, 32, 8) F(T, 1, 128, 4) \
+  F(T, 1, 512, 4) F(T, 1, 512, 8) F(T, 1, 1024, 16)
 
 cudaError_t launch_fwd(const Geo& g, const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                        cudaStream_t s) {
@@ -594,10 +602,10 @@ cudaError_t launch_fwd(const Geo& g, const void* x, const void* w, const void* b
   }
   if (g.bf16) {
     NORM_FWD_SHAPES(NORM_FWD, __nv_bfloat16, 8) NORM_FWD(__nv_bfloat16, 4, 32, 3)
-    NORM_ONE_SHAPES(NORM_FWD, __nv_bfloat16) NORM_FWD(__nv_bfloat16, 1, 128, 8)
+    NORM_ONE_SHAPES(NORM_FWD, __nv_bfloat16) NORM_FWD(__nv_bfloat16, 1, 128, 8) NORM_FWD(__nv_bfloat16, 1, 1024, 8)
   } else {
     NORM_FWD_SHAPES(NORM_FWD, float, 4) NORM_FWD(float, 4, 16, 3) NORM_FWD(float, 4, 1024, 4)
-    NORM_ONE_SHAPES(NORM_FWD, float) NORM_FWD(float, 1, 128, 8)
+    NORM_ONE_SHAPES(NORM_FWD, float) NORM_FWD(float, 1, 128, 8) NORM_FWD(float, 1, 1024, 8)
   }
   return cudaErrorInvalidValue;
 }
@@ -618,10 +626,10 @@ cudaError_t launch_bwd(const Geo& g, const void* x, const void* dy, const void* 
   }
   if (g.bf16) {
     NORM_BWD_SHAPES(NORM_BWD, __nv_bfloat16, 8) NORM_BWD(__nv_bfloat16, 4, 32, 3)
-    NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4)
+    NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4) NORM_BWD(__nv_bfloat16, 1, 512, 16)
   } else {
     NORM_BWD_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 16, 3) NORM_BWD(float, 4, 1024, 4)
-    NORM_ONE_SHAPES(NORM_BWD, float) NORM_BWD(float, 1, 256, 4)
+    NORM_ONE_SHAPES(NORM_BWD, float) NORM_BWD(float, 1, 256, 4) NORM_BWD(float, 1, 512, 16)
   }
   if (e != cudaSuccess || !part) return e;
   const dim3 fgrid((unsigned)((g.c + 31) / 32), (unsigned)g.groups, 2);

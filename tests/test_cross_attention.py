@@ -162,6 +162,54 @@ def test_broadcast_inputs(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("nq", [5, 90])
+def test_one_state_repeated_over_the_tokens(nq):
+    """A token stride of zero, which the tensor-core kernels do not take: the other path, the same results."""
+    gen = torch.Generator().manual_seed(10)
+    b, h, nk, d = 2, 8, 150, 64
+    q, g = (util.tokens(gen, b, h, nq, d, BF16) for _ in range(2))
+    k = util.tokens(gen, b, h, nk, d, BF16)
+    v = util.tokens(gen, b, h, 1, d, BF16).expand(b, h, nk, d)
+    p = llsa.CrossProblem(b, h, nq, nk, d)
+    op = llsa.CrossAttention(p)
+    op.forward(q, k, v)
+    op.backward_pass(q, k, v, g)
+    for name, (want, bound) in util.cross_reference(q, k, v, torch.ones(b, nk, dtype=torch.bool), p.scale, g).items():
+        util.check(name, getattr(op, name), want, bound)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq,nk", [(200, 70), (200, 300), (1, 300)])
+def test_offsets_beyond_32_bits(nq, nk):
+    """The second batch row of every tensor lies more than 2^31 elements behind the first."""
+    gen = torch.Generator().manual_seed(11)
+    b, h, d = 2, 2, 64
+    far = (1 << 31) + 4096
+    p = llsa.CrossProblem(b, h, nq, nk, d)
+    big = torch.empty(far + 8 * h * (nq + nk) * d, dtype=BF16, device="cuda")
+    at = 0
+
+    def place(shape):
+        nonlocal at
+        t = big.as_strided(shape, (far, shape[2] * d, d, 1), at)
+        at += h * shape[2] * d
+        return t
+
+    q, g, o, dq = (place(p.q_shape) for _ in range(4))
+    k, v, dk, dv = (place(p.k_shape) for _ in range(4))
+    for t in (q, g, k, v):
+        t.copy_(torch.randn(t.shape, generator=gen).to(BF16))
+    lse = torch.empty(p.q_shape[:3], device="cuda")
+    sizes = llsa.cross_query_sizes(p)
+    work = torch.empty(max(sizes["fwd_workspace_bytes"], sizes["bwd_workspace_bytes"]), dtype=torch.uint8, device="cuda")
+    llsa.cross_attn_fwd(p, q, k, v, o, lse, workspace=work)
+    llsa.cross_attn_bwd(p, q, k, v, o, g, lse, dq, dk, dv, workspace=work)
+    got = dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+    for name, (want, bound) in util.cross_reference(q, k, v, torch.ones(b, nk, dtype=torch.bool), p.scale, g).items():
+        util.check(name, got[name], want, bound)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_gradients_against_differences(dtype):
     """<dq, u> + <dk, s> + <dv, t> is the derivative of <O, dO> along (u, s, t), by central differences in 64 bits."""

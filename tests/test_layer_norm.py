@@ -106,6 +106,26 @@ def test_modulation_from_a_projection(pt, c, first):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("c", [64, 33])
+def test_offsets_beyond_32_bits(c):
+    gen = torch.Generator().manual_seed(12)
+    b, n = 2, 50
+    far = (1 << 31) + 4096
+    big = torch.empty(far + 4 * n * c, dtype=BF16, device="cuda")
+    x, y, dy, dx = (big.as_strided((b, 1, n, c), (far, n * c, c, 1), i * n * c) for i in range(4))
+    for t in (x, dy):
+        t.copy_(torch.randn(t.shape, generator=gen).to(BF16))
+    w = torch.randn(c, generator=gen).cuda()
+    p = llsa.NormProblem(b, 1, n, c, param_dtype=llsa.FP32)
+    mean, rstd = (torch.empty(b, 1, n, device="cuda") for _ in range(2))
+    llsa.layer_norm_fwd(p, x, w, None, y, mean, rstd)
+    llsa.layer_norm_bwd(p, x, dy, w, mean, rstd, dx=dx)
+    ref = util.norm_reference(x, w, None, p.eps, BF16, F32, False, dy)
+    util.check("y", y, *ref["y"])
+    util.check("dx", dx, *ref["dx"])
+
+
+@pytest.mark.gpu
 def test_constant_rows():
     """No variance: xhat is zero, y the bias; eps keeps the gradients finite."""
     p = llsa.NormProblem(1, 1, 4, 64, dtype=llsa.FP32)
