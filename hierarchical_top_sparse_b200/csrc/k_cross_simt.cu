@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Ge
   const int bh = (int)(blockIdx.x / ks / nqt);
   const int b = bh / g.h, h = bh % g.h, hk = h / g.group;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const bool busy = qt * BM + (int)(threadIdx.x >> 5) * 8 < g.nq;    // of the warp's eight queries
   const int n = key_count(g, keys, b);
   const uint8_t* mask = keys.mask ? keys.mask + (int64_t)b * g.nk : nullptr;
   const int ntiles = (n + BN - 1) / BN;
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Ge
     load_tile<T, DP, BN>(s.kt, LD, nullptr, kb, g.k.n, key0, n, g.d, mask);
     load_tile<T, DP, BN>(nullptr, 0, s.vn, vb, g.v.n, key0, n, g.d, mask);
     __syncthreads();
+    if (!busy) continue;                                 // (barriers count warps: the two above are all of a step)
     float z[4][4];
     product_4x4<DP>(z, s.qt + ty * 4, s.kt + tx * 4);
     bool ok[4];
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Ge
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       store4(s.pt + (tx * 4 + j) * LD + ty * 4, make_float4(z[0][j], z[1][j], z[2][j], z[3][j]));
-    __syncthreads();
+    __syncwarp();                                        // a warp's weights are its own rows'
     const int live = min(BN, n - key0);                  // the weights behind are zero
 #pragma unroll 4
     for (int key = 0; key < live; ++key) {
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Geo
   const int bh = (int)(blockIdx.x / ks / nqt);
   const int b = bh / g.h, h = bh % g.h, hk = h / g.group;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const bool busy = qt * BM + (int)(threadIdx.x >> 5) * 8 < g.nq;    // of the warp's eight queries
   const int n = key_count(g, keys, b);
   const uint8_t* mask = keys.mask ? keys.mask + (int64_t)b * g.nk : nullptr;
   const int ntiles = (n + BN - 1) / BN;
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Geo
     load_tile<T, DP, BN>(s.kt, LD, s.kn, kb, g.k.n, key0, n, g.d, mask);
     load_tile<T, DP, BN>(s.vt, LD, nullptr, vb, g.v.n, key0, n, g.d, mask);
     __syncthreads();
+    if (!busy) continue;
     float z[4][4], dp[4][4];
     product_4x4<DP>(z, s.qt + ty * 4, s.kt + tx * 4);
     product_4x4<DP>(dp, s.gt + ty * 4, s.vt + tx * 4);
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Geo
         x[i] = ok ? exp2f(fmaf(z[i][j], sc2, -ls[i])) * (dp[i][j] - dd[i]) * g.scale : 0.f;
       store4(s.st + (tx * 4 + j) * LD + ty * 4, make_float4(x[0], x[1], x[2], x[3]));
     }
-    __syncthreads();
+    __syncwarp();
     const int live = min(BN, n - key0);
 #pragma unroll 4
     for (int key = 0; key < live; ++key) {
@@ -498,8 +502,9 @@ __global__ void __launch_bounds__(THREADS) dkv_kernel(const __grid_constant__ Ge
       store4(s.ds + (tx * 2 + j) * LD + ty * 4, make_float4(ds[0], ds[1], ds[2], ds[3]));
     }
     __syncthreads();
+    const int live = min(BQ, g.nq - row0);
 #pragma unroll 2
-    for (int r = 0; r < BQ; ++r) {
+    for (int r = 0; r < live; ++r) {
       const float4 p = *reinterpret_cast<const float4*>(s.p + r * LD + ty * 4);
       const float4 e = *reinterpret_cast<const float4*>(s.ds + r * LD + ty * 4);
       const float ps[4] = {p.x, p.y, p.z, p.w}, es[4] = {e.x, e.y, e.z, e.w};
