@@ -47,7 +47,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
-// A whole warp waits for a barrier, at most 2 s: all lanes ask, and go on or
+// A whole warp waits for a barrier, at most 4 s (the longest wait of a run that
+// goes well, the epilogue's for an item of the most tiles, stays under 2 s): all lanes ask, and go on or
 // give up together.  The vote before the branch keeps the ready case short
 // (about 70 cycles; a branch on each lane's own answer took about 190, and one
 // lane asking for all of them longer still).
@@ -62,7 +63,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));    // (wraps after 4.3 s)
     now = __shfl_sync(0xffffffffu, now, 0);
     if (n == 64u) t0 = now;
-    if (now - t0 > 2000000000u) return false;
+    if (now - t0 > 4000000000u) return false;
   }
 }
 
@@ -76,7 +77,7 @@ __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
     uint32_t now;
     asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
     if (n == 64u) t0 = now;
-    if (now - t0 > 2000000000u) return false;
+    if (now - t0 > 4000000000u) return false;
   }
   return true;
 }

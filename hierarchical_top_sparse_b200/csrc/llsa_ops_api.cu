@@ -73,7 +73,9 @@ static llsa_status make_cross(const llsa_cross_problem* p, cross::Geo* g) {
   if (!(p->scale >= 0.0f) || isinf(p->scale)) return LLSA_ERR_ARG;
   if (p->d % 8 != 0 || p->d > 128) return LLSA_ERR_UNSUPPORTED;
   const int64_t b = p->batch, h = p->heads, hk = p->kv_heads, nq = p->nq, nk = p->nk, d = p->d;
-  if (b * h > (1 << 24) || nq > (1 << 30) || nk > (1 << 30)) return LLSA_ERR_SHAPE;
+  if (b * h > (1 << 24) || nq > LLSA_CROSS_MAX_TOKENS || nk > LLSA_CROSS_MAX_TOKENS) return LLSA_ERR_SHAPE;
+  // a block's work between two hand-offs ends well before their waits give up
+  if (h / hk * nq > 4ll * LLSA_CROSS_MAX_TOKENS) return LLSA_ERR_SHAPE;
   if (b * h * nq >= (1ll << 34) || b * hk * nk >= (1ll << 34)) return LLSA_ERR_SHAPE;
   // one block per 32 queries or keys and head at most: a grid of fewer than 2^31 blocks
   if (b * h * ((nq + 31) / 32) >= (1ll << 31) || b * hk * ((nk + 31) / 32) >= (1ll << 31)) return LLSA_ERR_SHAPE;

@@ -249,7 +249,10 @@ typedef struct {
 } llsa_strides;
 
 /* Cross attention: `nq` queries per head and batch row attend to the `nk`
- * states of an encoder. */
+ * states of an encoder; at most LLSA_CROSS_MAX_TOKENS of each, and four times as
+ * many queries in the heads that share a key head. */
+#define LLSA_CROSS_MAX_TOKENS (1 << 24)
+
 typedef struct {
   int batch, heads;       /* of the queries */
   int kv_heads;           /* of keys and values; divides heads: query head h reads key head h / (heads / kv_heads) */

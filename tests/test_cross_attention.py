@@ -365,7 +365,8 @@ def problem(**kw):
     (dict(batch=0), 1), (dict(heads=0), 1), (dict(kv_heads=3), 1), (dict(kv_heads=0), 1), (dict(kv_heads=8), 1),
     (dict(nq=0), 1), (dict(nk=0), 1), (dict(dtype=2), 1), (dict(scale=-1.0), 1), (dict(scale=math.inf), 1),
     (dict(scale=math.nan), 1), (dict(d=0, scale=1.0), 1), (dict(d=60), 7), (dict(d=136), 7),
-    (dict(nq=1 << 30, heads=1 << 20, kv_heads=1), 2), (dict(batch=1 << 13, heads=1 << 13), 2),
+    (dict(nq=1 << 24), 0), (dict(nk=1 << 24), 0), (dict(nq=(1 << 24) + 1), 2), (dict(nk=(1 << 24) + 1), 2),
+    (dict(nq=1 << 24, heads=16, kv_heads=1), 2), (dict(nq=1 << 30, heads=1 << 20, kv_heads=1), 2), (dict(batch=1 << 13, heads=1 << 13), 2),
 ])
 def test_validation(kw, status):
     assert llsa.cross_validate(problem(**kw)) == status
