@@ -7,8 +7,8 @@
 // Bound by memory: every row is read once and kept in registers as it came (the
 // variance is the mean of the squared deviations from the mean, in a second
 // pass over the registers, so that large offsets cost no digits).  G threads
-// work on a row, each on IT vectors of 16 bytes (single values where the width,
-// a stride or an address does not allow vectors); rows of up to 2 KB take a
+// work on a row, each on IT vectors of 16 bytes (narrower ones, down to single
+// values, where the width, a stride or an address does not allow them); rows of up to 2 KB take a
 // part of a warp or a warp, wider ones a block.  R rows are taken at a time,
 // and the next R are on their way while these are worked on: an SM needs some
 // 40 KB in flight.  Rows are walked in the order of x's memory.
@@ -28,6 +28,8 @@ namespace norm {
 template <typename T, int V> struct Raw;
 template <> struct Raw<__nv_bfloat16, 8> { uint4 w; };
 template <> struct Raw<__nv_bfloat16, 4> { uint2 w; };
+template <> struct Raw<__nv_bfloat16, 2> { uint32_t w; };
+template <> struct Raw<float, 2> { float2 w; };
 template <> struct Raw<float, 4> { float4 w; };
 template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 w; };
 template <> struct Raw<float, 1> { float w; };
@@ -52,6 +54,14 @@ __device__ __forceinline__ void unpack(const Raw<float, 4>& r, float* f) {
   f[2] = r.w.z;
   f[3] = r.w.w;
 }
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 2>& r, float* f) {
+  f[0] = __uint_as_float(r.w << 16);
+  f[1] = __uint_as_float(r.w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(const Raw<float, 2>& r, float* f) {
+  f[0] = r.w.x;
+  f[1] = r.w.y;
+}
 __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 1>& r, float* f) { f[0] = __bfloat162float(r.w); }
 __device__ __forceinline__ void unpack(const Raw<float, 1>& r, float* f) { f[0] = r.w; }
 
@@ -66,6 +76,8 @@ __device__ __forceinline__ void pack(Raw<__nv_bfloat16, 4>& r, const float* f) {
   r.w = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
 }
 __device__ __forceinline__ void pack(Raw<float, 4>& r, const float* f) { r.w = make_float4(f[0], f[1], f[2], f[3]); }
+__device__ __forceinline__ void pack(Raw<__nv_bfloat16, 2>& r, const float* f) { r.w = pack2(f[0], f[1]); }
+__device__ __forceinline__ void pack(Raw<float, 2>& r, const float* f) { r.w = make_float2(f[0], f[1]); }
 __device__ __forceinline__ void pack(Raw<__nv_bfloat16, 1>& r, const float* f) { r.w = __float2bfloat16_rn(f[0]); }
 __device__ __forceinline__ void pack(Raw<float, 1>& r, const float* f) { r.w = f[0]; }
 
@@ -84,6 +96,10 @@ __device__ __forceinline__ void load_param(const void* p, int bf16, int64_t at, 
       f[1] = __uint_as_float(u.x & 0xffff0000u);
       f[2] = __uint_as_float(u.y << 16);
       f[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else if constexpr (V == 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(w);
+      f[0] = __uint_as_float(u << 16);
+      f[1] = __uint_as_float(u & 0xffff0000u);
     } else {
       f[0] = __bfloat162float(*w);
     }
@@ -98,6 +114,10 @@ __device__ __forceinline__ void load_param(const void* p, int bf16, int64_t at, 
         f[i + 2] = u.z;
         f[i + 3] = u.w;
       }
+    } else if constexpr (V == 2) {
+      const float2 u = *reinterpret_cast<const float2*>(w);
+      f[0] = u.x;
+      f[1] = u.y;
     } else {
       f[0] = *w;
     }
@@ -166,9 +186,9 @@ template <int G> constexpr int threads() { return G <= 32 ? 256 : G; }
 // Rows of a step and thread group.  Two where a thread holds one vector of each (with four the registers leave too few
 // blocks: 51 us against 44 for 786432 rows of 64 bf16 channels).
 template <int G, int IT, int V> constexpr int rows_at_once() {
-  if (V > 1) return G > 32 || IT > 1 ? 1 : 2;
   if (G > 32) return 1;
-  return IT <= 2 ? 4 : (IT <= 4 ? 2 : 1);
+  if (V <= 2) return IT <= 2 ? 4 : (IT <= 4 ? 2 : 1);
+  return IT > 1 ? 1 : 2;
 }
 
 template <typename T, int V, int G, int IT>
@@ -312,7 +332,8 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
                                                            const float* __restrict__ rstd, T* dx,
                                                            float* __restrict__ part) {
   constexpr int RPB = threads<G>() / G;
-  constexpr int R = V > 1 ? (G > 32 || IT > 1 ? 1 : 2) : (G > 32 ? (G == 128 ? 2 : 1) : (IT <= 2 ? 4 : (IT <= 4 ? 2 : 1)));
+  constexpr int R = G > 32 ? (V == 1 && G == 128 ? 2 : 1)
+                           : (V <= 2 ? (IT <= 2 ? 4 : (IT <= 4 ? 2 : 1)) : (IT > 1 ? 1 : 2));
   constexpr int NV = IT * V;
   __shared__ float red[G > 32 ? 2 * 2 * R * 32 : 1];
   __shared__ float cols[G <= 32 ? 8 * G * NV : 1];   // a block's eight warps' sums
@@ -522,7 +543,8 @@ __global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ 
 
 // ------------------------------------------------------------------ host
 
-// Values per load, threads per row and loads per thread.  A row's threads are
+// Values per load (16 bytes, or what a width, stride or address that is no
+// multiple of that allows), threads per row and loads per thread.  A row's threads are
 // the fewest that hold it in a few registers: in the backward, which keeps two
 // sums for each channel of a thread, about 16 channels each, in the forward up
 // to 32.  257 to 384 bf16 channels take 8-byte loads, which fill a warp where
@@ -532,8 +554,8 @@ struct Shape {
   int v, g, it;
 };
 static Shape shape_of(const Geo& g, bool bwd) {
-  if (g.vec) {
-    const int v = g.bf16 ? 8 : 4, n = g.c / v;
+  if (g.vec * (g.bf16 ? 2 : 4) == 16) {
+    const int v = g.vec, n = g.c / v;
     if (n <= 8) return {v, 8, 1};
     if (n <= 16) return {v, 16, 1};
     if (n <= 32) return {v, 32, 1};
@@ -552,6 +574,20 @@ static Shape shape_of(const Geo& g, bool bwd) {
     if (n <= 1024) return {v, 512, 2};
     if (n <= 2048) return {v, 512, 4};
     return {v, 1024, 4};
+  }
+  if (g.vec > 1) {                             // 8-byte loads of bf16, or pairs
+    const int v = g.vec, n = g.c / v;
+    if (n <= 8) return {v, 8, 1};
+    if (n <= 16) return {v, 8, 2};
+    if (n <= 32) return {v, 8, 4};
+    if (n <= 64) return {v, 16, 4};
+    if (n <= 128) return {v, 32, 4};
+    if (n <= 256) return {v, 128, 2};
+    if (n <= 512) return {v, 128, 4};
+    if (n <= 1024) return {v, 256, 4};
+    if (n <= 2048) return {v, 512, 4};
+    if (n <= 4096) return {v, 512, 8};
+    return {v, 1024, 8};
   }
   if (g.c <= 8) return {1, 8, 1};
   if (g.c <= 16) return {1, 8, 2};
@@ -583,6 +619,9 @@ int bwd_parts(const Geo& g) {
   F(T, V, 8, 1) F(T, V, 16, 1) F(T, V, 32, 1) F(T, V, 32, 2) F(T, V, 512, 2) F(T, V, 512, 4)
 #define NORM_FWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 32, 3) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 256, 2)
 #define NORM_BWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 128, 1) F(T, V, 256, 1) F(T, V, 512, 1)
+#define NORM_FEW_SHAPES(F, T, V) \
+  F(T, V, 8, 1) F(T, V, 8, 2) F(T, V, 8, 4) F(T, V, 16, 4) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 128, 4) \
+  F(T, V, 256, 4) F(T, V, 512, 4) F(T, V, 512, 8)
 #define NORM_ONE_SHAPES(F, T) \
   F(T, 1, 8, 1) F(T, 1, 8, 2) F(T, 1, 8, 4) F(T, 1, 8, 8) F(T, 1, 16, 8) F(T, 1, 32, 8) F(T, 1, 128, 4) \
   F(T, 1, 512, 4) F(T, 1, 512, 8) F(T, 1, 1024, 16)
@@ -603,9 +642,12 @@ cudaError_t launch_fwd(const Geo& g, const void* x, const void* w, const void* b
   }
   if (g.bf16) {
     NORM_FWD_SHAPES(NORM_FWD, __nv_bfloat16, 8) NORM_FWD(__nv_bfloat16, 4, 32, 3)
+    NORM_FEW_SHAPES(NORM_FWD, __nv_bfloat16, 4) NORM_FEW_SHAPES(NORM_FWD, __nv_bfloat16, 2)
+    NORM_FWD(__nv_bfloat16, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_FWD, __nv_bfloat16) NORM_FWD(__nv_bfloat16, 1, 128, 8) NORM_FWD(__nv_bfloat16, 1, 1024, 8)
   } else {
     NORM_FWD_SHAPES(NORM_FWD, float, 4) NORM_FWD(float, 4, 16, 3) NORM_FWD(float, 4, 1024, 4)
+    NORM_FEW_SHAPES(NORM_FWD, float, 2) NORM_FWD(float, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_FWD, float) NORM_FWD(float, 1, 128, 8) NORM_FWD(float, 1, 1024, 8)
   }
   return cudaErrorInvalidValue;
@@ -627,9 +669,12 @@ cudaError_t launch_bwd(const Geo& g, const void* x, const void* dy, const void* 
   }
   if (g.bf16) {
     NORM_BWD_SHAPES(NORM_BWD, __nv_bfloat16, 8) NORM_BWD(__nv_bfloat16, 4, 32, 3)
+    NORM_FEW_SHAPES(NORM_BWD, __nv_bfloat16, 4) NORM_FEW_SHAPES(NORM_BWD, __nv_bfloat16, 2)
+    NORM_BWD(__nv_bfloat16, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4) NORM_BWD(__nv_bfloat16, 1, 512, 16)
   } else {
     NORM_BWD_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 16, 3) NORM_BWD(float, 4, 1024, 4)
+    NORM_FEW_SHAPES(NORM_BWD, float, 2) NORM_BWD(float, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_BWD, float) NORM_BWD(float, 1, 256, 4) NORM_BWD(float, 1, 512, 16)
   }
   if (e != cudaSuccess || !part) return e;

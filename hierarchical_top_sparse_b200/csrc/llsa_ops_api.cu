@@ -14,10 +14,11 @@ constexpr int kSms = 148;                       // sizes follow from the problem
 
 static bool aligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
-static bool vectors(std::initializer_list<const void*> all) {
+// The widest load of up to v values of `size` bytes that every address allows.
+static int widest(int v, size_t size, std::initializer_list<const void*> all) {
   for (const void* p : all)
-    if (!aligned(p, 16)) return false;
-  return true;
+    while (v > 1 && !aligned(p, v * size > 16 ? 16 : v * size)) v /= 2;
+  return v;
 }
 
 struct Dim {
@@ -127,18 +128,18 @@ static llsa_status make_norm(const llsa_norm_problem* p, norm::Geo* g) {
   st[4][1] = n;
   st[4][2] = 1;
   const int64_t size[3] = {b, h, n};
-  const int64_t m = p->dtype == LLSA_BF16 ? 8 : 4;
-  g->vec = c % m == 0;
+  g->vec = p->dtype == LLSA_BF16 ? 8 : 4;
+  while (c % g->vec) g->vec /= 2;
   for (int t = 0; t < 4; ++t)
     for (int i = 0; i < 3; ++i)
-      if (size[i] > 1 && st[t][i] % m) g->vec = 0;
+      while (size[i] > 1 && st[t][i] % g->vec) g->vec /= 2;
   g->ws = g->bs = p->c;
   if (p->per_batch) {
     if (p->weight_batch < 0 || p->bias_batch < 0) return LLSA_ERR_ARG;
     if (p->weight_batch >= (1ll << 37) || p->bias_batch >= (1ll << 37)) return LLSA_ERR_SHAPE;
     if (p->weight_batch) g->ws = p->weight_batch;
     if (p->bias_batch) g->bs = p->bias_batch;
-    if (b > 1 && (g->ws % 8 || g->bs % 8)) g->vec = 0;
+    while (b > 1 && (g->ws % g->vec || g->bs % g->vec)) g->vec /= 2;
   }
   int64_t* out[5] = {g->x, g->y, g->dy, g->dx, g->s};
   // the loops over the group's rows, outermost first, in the order of x's strides; loops of one drop out
@@ -311,7 +312,7 @@ llsa_status llsa_layer_norm_fwd(const llsa_norm_problem* p, const void* x, const
   LLSA_MAY(bias, pt);
   LLSA_MAY(mean, 4);
   LLSA_MAY(rstd, 4);
-  if (!llsa::vectors({x, y, weight, bias})) g.vec = 0;
+  g.vec = llsa::widest(llsa::widest(g.vec, t, {x, y}), pt, {weight, bias});
   return llsa::launched(llsa::norm::launch_fwd(g, x, weight, bias, y, mean, rstd, (cudaStream_t)stream));
 }
 
@@ -329,7 +330,7 @@ llsa_status llsa_layer_norm_bwd(const llsa_norm_problem* p, const void* x, const
   LLSA_MAY(dbias, pt);
   LLSA_MAY(mean, 4);
   LLSA_MAY(rstd, 4);
-  if (!llsa::vectors({x, dy, dx, weight})) g.vec = 0;
+  g.vec = llsa::widest(llsa::widest(g.vec, t, {x, dy, dx}), pt, {weight});
   if (!dx && !dweight && !dbias) return LLSA_ERR_ARG;
   if (dweight || dbias) LLSA_NEED(workspace);
   return llsa::launched(

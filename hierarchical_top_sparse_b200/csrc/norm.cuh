@@ -22,7 +22,7 @@ struct Geo {
   int c;
   float eps;
   int bf16, param_bf16;
-  int vec;                   // 16-byte vectors throughout (c, every stride and every address allow it)
+  int vec;                   // values a load: the most, up to 16 bytes, that c, every stride and every address allow
 };
 
 constexpr int kSms = 148;
@@ -32,7 +32,7 @@ constexpr int kSms = 148;
 int bwd_parts(const Geo& g);
 inline size_t bwd_work_bytes(Geo g) {
   int most = 0;
-  for (g.vec = 0; g.vec < 2; ++g.vec) most = bwd_parts(g) > most ? bwd_parts(g) : most;
+  for (g.vec = g.bf16 ? 8 : 4; g.vec; g.vec /= 2) most = bwd_parts(g) > most ? bwd_parts(g) : most;
   return (size_t)g.groups * most * 2 * g.c * sizeof(float);
 }
 

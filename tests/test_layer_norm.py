@@ -38,7 +38,7 @@ def run_case(dtype, pt, b, h, n, c, layout="bhnd", per_batch=False, weight=True,
 TYPES = [(BF16, BF16), (BF16, F32), (F32, F32)]
 # every width at which the kernels change their shape, its neighbours, and odd ones
 WIDTHS = [1, 2, 7, 8, 9, 17, 32, 33, 45, 64, 72, 100, 127, 128, 129, 256, 257, 264, 384, 388, 512, 520, 768, 1000, 1001, 1024,
-          1032, 1152, 2048, 2056, 4096, 4104, 5001, 8192, 8200, 16383, 16384, 301, 777, 1501, 3001, 9001]
+          1032, 1152, 2048, 2056, 4096, 4104, 5001, 8192, 8200, 16383, 16384, 301, 777, 1501, 3001, 9001, 12, 20, 50, 92, 154, 244, 330, 602, 1012, 1514, 3010, 6004, 10002]
 
 
 @pytest.mark.gpu
