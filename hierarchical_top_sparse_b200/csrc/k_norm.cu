@@ -562,6 +562,8 @@ static Shape shape_of(const Geo& g, bool bwd) {
     if (n <= 48) return g.bf16 ? Shape{4, 32, 3} : Shape{4, 16, 3};
     if (n <= 64) return {v, 32, 2};
     if (bwd) {
+      if (!g.bf16 && n <= 96) return {v, 32, 3};
+      if (!g.bf16 && n <= 128) return {v, 32, 4};
       if (n <= 128) return {v, 128, 1};
       if (n <= 256) return {v, 256, 1};
       if (n <= 512) return {v, 512, 1};
@@ -673,7 +675,7 @@ cudaError_t launch_bwd(const Geo& g, const void* x, const void* dy, const void* 
     NORM_BWD(__nv_bfloat16, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4) NORM_BWD(__nv_bfloat16, 1, 512, 16)
   } else {
-    NORM_BWD_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 16, 3) NORM_BWD(float, 4, 1024, 4)
+    NORM_BWD_SHAPES(NORM_BWD, float, 4) NORM_BWD(float, 4, 16, 3) NORM_BWD(float, 4, 32, 3) NORM_BWD(float, 4, 32, 4) NORM_BWD(float, 4, 1024, 4)
     NORM_FEW_SHAPES(NORM_BWD, float, 2) NORM_BWD(float, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_BWD, float) NORM_BWD(float, 1, 256, 4) NORM_BWD(float, 1, 512, 16)
   }
