@@ -332,7 +332,10 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
                                                            const float* __restrict__ rstd, T* dx,
                                                            float* __restrict__ part) {
   constexpr int RPB = threads<G>() / G;
-  constexpr int R = G > 32 ? (V == 1 && G == 128 ? 2 : 1)
+  // Rows of a step and thread group.  Block-wide rows: two a barrier where that paid (50 M bf16 values, 768, 1024, 4096
+  // channels: 131, 112, 129 us against 155, 124, 156; 2048 channels 116 against 103, 25 M fp32 values of 1024 124
+  // against 86).
+  constexpr int R = G > 32 ? ((V == 1 && G == 128) || (V == 8 && IT == 1 && G != 256) ? 2 : 1)
                            : (V <= 2 ? (IT <= 2 ? 4 : (IT <= 4 ? 2 : 1)) : (IT > 1 ? 1 : 2));
   constexpr int NV = IT * V;
   __shared__ float red[G > 32 ? 2 * 2 * R * 32 : 1];
