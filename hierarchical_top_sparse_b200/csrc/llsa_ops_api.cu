@@ -242,6 +242,7 @@ llsa_status llsa_cross_attn_fwd(const llsa_cross_problem* p, const void* q, cons
   LLSA_NEED(o);
   LLSA_MAY(kv_len, 4);
   LLSA_MAY(lse, 16);
+  LLSA_MAY(workspace, 16);                      // of any call that is given one, whether its plan needs it or not
   const llsa::cross::Keys keys{kv_len, key_mask};
   if (llsa::cross::token_supported(g)) {
     LLSA_NEED(workspace);
@@ -332,6 +333,7 @@ llsa_status llsa_layer_norm_bwd(const llsa_norm_problem* p, const void* x, const
   LLSA_MAY(rstd, 4);
   g.vec = llsa::widest(llsa::widest(g.vec, t, {x, dy, dx}), pt, {weight});
   if (!dx && !dweight && !dbias) return LLSA_ERR_ARG;
+  LLSA_MAY(workspace, 16);
   if (dweight || dbias) LLSA_NEED(workspace);
   return llsa::launched(
       llsa::norm::launch_bwd(g, x, dy, weight, mean, rstd, dx, dweight, dbias, workspace, (cudaStream_t)stream));

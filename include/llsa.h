@@ -234,9 +234,10 @@ llsa_status llsa_selftest_wait_timeout(unsigned limit_us, int code, int arrive, 
  * llsa_strides of zeros means the contiguous layout above.  An input may
  * repeat itself (a stride of 0); tensors that are written may not overlap
  * themselves (LLSA_ERR_ARG), nor any other argument unless a call says so.
- * The buffers of cross attention and all workspaces are 16-byte aligned; those
- * of layer norm need their element's alignment only (with 16 bytes, and widths
- * and strides that are multiples of 8 elements, it is faster).
+ * The buffers of cross attention and all workspaces are 16-byte aligned (a
+ * workspace that is given is checked even where the call has no use for it);
+ * the tensors of layer norm need their element's alignment only (with 16 bytes,
+ * and widths and strides that are multiples of 8 elements, it is faster).
  * The conventions at the top of this file hold otherwise: asynchronous on
  * `stream`, on the current device, which owns every buffer; nothing is
  * allocated and nothing kept.  A workspace may be used by one call at a time
