@@ -411,11 +411,12 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
     }
     fetch(r0 + step);
     float sum[2 * R];
-    f2 shift[R], scale[R];                             // xhat = x rstd - mean rstd
+    // xhat = (x - mean) rstd, as in the forward: x rstd - mean rstd would leave the rounding of mean rstd in rows far from 0
+    f2 minus[R], scale[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       scale[k] = twice(rs[k]);
-      shift[k] = twice(-mu[k] * rs[k]);
+      minus[k] = V == 1 ? pair(-mu[k], 0.f) : twice(-mu[k]);
       f2 s0 = twice(0.f), s1 = twice(0.f);
       const bool live = r0 + k * RPB + slot < g.rows;
 #pragma unroll
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
           weights_of(i, ww);
 #pragma unroll
           for (int e = 0; e < P; ++e) {
-            const f2 xh = fma2(fx[e], scale[k], shift[k]), gw = mul2(fg[e], ww[e]);
+            const f2 xh = mul2(add2(fx[e], minus[k]), scale[k]), gw = mul2(fg[e], ww[e]);
             s0 = add2(s0, gw);
             s1 = fma2(gw, xh, s1);
             dw[i * P + e] = fma2(fg[e], xh, dw[i * P + e]);
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
           weights_of(i, ww);
 #pragma unroll
           for (int e = 0; e < P; ++e) {
-            const f2 xh = fma2(fx[e], scale[k], shift[k]);
+            const f2 xh = mul2(add2(fx[e], minus[k]), scale[k]);
             fx[e] = fma2(fma2(xh, c2, mul2(fg[e], ww[e])), scale[k], c1);   // rstd (g - xhat c2) - rstd c1
           }
           Raw<T, V> o;
