@@ -534,8 +534,9 @@ __global__ void __launch_bounds__(THREADS) dkv_kernel(const __grid_constant__ Ge
     for (int j = 0; j < DP / 64; ++j) {
       const int c = 64 * j + tx * 4;
       if (c >= g.d) continue;
-      const float4 x = make_float4(ak[i][j][0], ak[i][j][1], ak[i][j][2], ak[i][j][3]);
-      const float4 y = make_float4(av[i][j][0], av[i][j][1], av[i][j][2], av[i][j][3]);
+      float4 x = make_float4(ak[i][j][0], ak[i][j][1], ak[i][j][2], ak[i][j][3]);
+      float4 y = make_float4(av[i][j][0], av[i][j][1], av[i][j][2], av[i][j][3]);
+      if (!ok[i]) x = y = make_float4(0.f, 0.f, 0.f, 0.f);   // (whatever its zero weights met)
       if (qs > 1) {
         const int64_t at = ((int64_t)split * keys_of(g) + (int64_t)bk * g.nk + key) * g.d + c;
         store4(partk + at, x);
