@@ -279,13 +279,16 @@ bwd_one_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         int h, n;
         const bool live = row_of(a, x.hk, x.u0 + i, row, h, n);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + x.b * g.dq.b + h * g.dq.h + n * g.dq.n;
+        // a query whose keys are all masked has gradient zero, whatever its zero weights met
+        bool any = true;
+        if (a.keys.mask && live) any = a.lse[((int64_t)x.b * g.h + h) * g.nq + n] != -INFINITY;
         if (!none) {
           if (!wait(&s.dq_full, tc_ & 1, 106)) break;
           tc::fence_after_sync();
           ++tc_;
         }
 #pragma unroll 1
-        for (int c = 0; c < c16; ++c) store(C::DQ, c, none, true, g.scale, out, nullptr, live);
+        for (int c = 0; c < c16; ++c) store(C::DQ, c, none, any, g.scale, out, nullptr, live);
         if (!none) {
           tc::fence_before_sync();
           arrive(&s.dq_free);

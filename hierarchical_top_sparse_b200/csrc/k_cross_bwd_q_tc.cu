@@ -229,13 +229,17 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
       int h, n;
       const bool live = row_of(a, x, sub * 32 + lane, h, n);
       const bool none = x.n == 0;
+      const int64_t at = ((int64_t)x.b * g.h + h) * g.nq + n;
+      // a query whose keys are all masked has gradient zero, whatever its zero weights met
+      bool any = true;
+      if (a.keys.mask && live) any = a.lse[at] != -INFINITY;
       if (!none) {
         if (!wait(&s.dq_full, ic & 1, 123)) break;
         tc::fence_after_sync();
         ++ic;
       }
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + x.b * g.dq.b + h * g.dq.h + n * g.dq.n;
-      float* part = a.part + ((int64_t)x.split * rows_of(g) + ((int64_t)x.b * g.h + h) * g.nq + n) * g.d;
+      float* part = a.part + ((int64_t)x.split * rows_of(g) + at) * g.d;
 #pragma unroll 1
       for (int c = 0; c < c16; ++c) {
         uint32_t w[16];
@@ -245,7 +249,7 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         }
         float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = none ? 0.f : __uint_as_float(w[e]) * g.scale;
+        for (int e = 0; e < 16; ++e) f[e] = none || !any ? 0.f : __uint_as_float(w[e]) * g.scale;
         if (live) store16(f, a.ks > 1 ? nullptr : out + 16 * c, part + 16 * c, 16 * c + 8 < g.d);
         __syncwarp();
       }

@@ -1,5 +1,5 @@
-"""Where nothing attends, nothing comes out: keys that are not valid have gradients of zero, whatever the queries and the
-upstream gradient hold."""
+"""Where nothing attends, nothing comes out: keys that are not valid have gradients of zero, and queries without a valid
+key o = 0, lse = -inf and dq = 0, whatever the queries and the upstream gradient hold."""
 import math
 
 import pytest
@@ -66,3 +66,26 @@ def test_keys_that_are_not_valid(dtype, repeated, how, value, size):
     bad = ~util.valid_keys(b, nk, kv_len, key_mask).cuda()
     for t in (op.dk, op.dv):
         assert bool((t.masked_select(bad[:, None, :, None]) == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,repeated", [(BF16, False), (BF16, True), (F32, False)])
+@pytest.mark.parametrize("how", ["length", "mask"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("size", SIZES)
+def test_queries_without_a_key(dtype, repeated, how, value, size):
+    """Batch rows without a valid key, their queries and upstream gradients not finite; the row with keys as the formulas."""
+    b, h, hk, nq, nk, d = size
+
+    def spoil(q, g):
+        q[1:, :, ::2] = value
+        g[1:, :, ::3] = value
+
+    kv_len, key_mask = keys_of(b, nk, how)
+    op = run(dtype, size, kv_len, key_mask, spoil, repeated)
+    clean = run(dtype, size, kv_len, key_mask, lambda q, g: None, repeated)
+    assert bool((op.o[1:] == 0).all()) and bool((op.lse[1:] == -math.inf).all())
+    for t in (op.dq, op.dk, op.dv):
+        assert bool((t[1:] == 0).all())
+    for name in ("o", "lse", "dq", "dk", "dv"):
+        assert torch.equal(getattr(op, name), getattr(clean, name)), name
