@@ -514,10 +514,17 @@ def cross_query_sizes(p: CrossProblem) -> dict:
     return {name: getattr(s, name) for name, _ in CCrossBuffers._fields_}
 
 
-def cross_attn_paths(p: CrossProblem) -> dict:
-    """Which kernels cross_attn_fwd / cross_attn_bwd run for p: "tensor" or "cuda-core"."""
+def cross_attn_paths(p: CrossProblem, q=None, k=None, v=None, dO=None) -> dict:
+    """Which kernels cross_attn_fwd / cross_attn_bwd run for p and tensors with these strides (contiguous ones where none
+    is given): "tensor", which the kernels for few queries are too, or "cuda-core"."""
+    c = p.c()
+    for name, field, x, shape in (("q", c.q, q, p.q_shape), ("k", c.k, k, p.k_shape), ("v", c.v, v, p.k_shape),
+                                  ("dO", c.d_o, dO, p.q_shape)):
+        if x is not None:
+            _checked(name, x, shape, _torch_dtype(p.dtype), x.device)
+            field.batch, field.head, field.token = _strides(name, x)
     f, b = ctypes.c_int(0), ctypes.c_int(0)
-    _check(lib().llsa_cross_attn_paths(ctypes.byref(p.c()), ctypes.byref(f), ctypes.byref(b)), "cross_attn_paths")
+    _check(lib().llsa_cross_attn_paths(ctypes.byref(c), ctypes.byref(f), ctypes.byref(b)), "cross_attn_paths")
     name = {1: "tensor", 0: "cuda-core"}
     return {"fwd": name[f.value], "bwd": name[b.value]}
 

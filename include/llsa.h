@@ -299,8 +299,10 @@ llsa_status llsa_cross_attn_bwd(const llsa_cross_problem* p, const void* q, cons
                                 const float* lse, void* dq, void* dk, void* dv, void* workspace,
                                 llsa_stream stream);
 
-/* Which kernels the two calls run for *p (host only, no launch): 1 for the
- * tensor-core kernels, 0 for the CUDA-core ones.  Either pointer may be NULL. */
+/* Which kernels the two calls run for *p, its strides among it (host only, no
+ * launch): 1 for the tensor-core kernels, 0 for the CUDA-core ones (fp32, and
+ * bf16 with a token stride of 0 in q, k, v or, backward, d_o; the forward for
+ * few queries takes those too).  Either pointer may be NULL. */
 llsa_status llsa_cross_attn_paths(const llsa_cross_problem* p, int* fwd_tc, int* bwd_tc);
 
 /* Layer norm of every token row over its c channels. */

@@ -1,0 +1,49 @@
+"""Which kernels cross attention runs, by size, type and strides, and the CUDA-core kernels in bf16."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from hierarchical_top_sparse_b200 import llsa  # noqa: E402
+import operators_util as util  # noqa: E402
+
+BF16, F32 = torch.bfloat16, torch.float32
+NUMBER = {BF16: llsa.BF16, F32: llsa.FP32}
+TENSOR, CUDA = {"fwd": "tensor", "bwd": "tensor"}, {"fwd": "cuda-core", "bwd": "cuda-core"}
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(nq=1), dict(nk=1), dict(nk=129), dict(d=8), dict(d=128, nk=4096), dict(kv_heads=1),
+                                dict(nq=4, kv_heads=1), dict(batch=3000, nq=1), dict(nq=65536)])
+def test_the_type_decides(kw):
+    base = dict(batch=2, heads=4, nq=200, nk=100)
+    base.update(kw)
+    assert llsa.cross_attn_paths(llsa.CrossProblem(**base)) == TENSOR
+    assert llsa.cross_attn_paths(llsa.CrossProblem(**base, dtype=llsa.FP32)) == CUDA
+
+
+@pytest.mark.parametrize("nq", [5, 200])
+def test_strides_decide(nq):
+    """A token stride of zero goes to the CUDA cores, other strides do not; few queries run by plain loads of any stride."""
+    p = llsa.CrossProblem(2, 4, nq, 100, 64)
+
+    def made(shape, layout):
+        b, h, n, d = shape
+        if layout == "repeated":
+            return torch.empty(b, h, 1, d, dtype=BF16).expand(shape)
+        if layout == "bnhd":
+            return torch.empty(b, n, h, d, dtype=BF16).transpose(1, 2)
+        if layout == "one image":
+            return torch.empty(1, h, n, d, dtype=BF16).expand(shape)
+        return torch.empty(shape, dtype=BF16)
+
+    shapes = dict(q=p.q_shape, k=p.k_shape, v=p.k_shape, dO=p.q_shape)
+    for layout in ("plain", "bnhd", "one image"):
+        assert llsa.cross_attn_paths(p, **{n: made(s, layout) for n, s in shapes.items()}) == TENSOR, layout
+    few = nq == 5
+    for name, shape in shapes.items():
+        got = llsa.cross_attn_paths(p, **{name: made(shape, "repeated")})
+        assert got["bwd"] == "cuda-core", name
+        assert got["fwd"] == ("tensor" if few or name == "dO" else "cuda-core"), name
+    with pytest.raises(ValueError, match="shape"):
+        llsa.cross_attn_paths(p, q=made(p.k_shape, "plain"))
