@@ -47,3 +47,34 @@ def test_strides_decide(nq):
         assert got["fwd"] == ("tensor" if few or name == "dO" else "cuda-core"), name
     with pytest.raises(ValueError, match="shape"):
         llsa.cross_attn_paths(p, q=made(p.k_shape, "plain"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 72, 128])
+@pytest.mark.parametrize("h,hk", [(3, 3), (4, 2)])
+@pytest.mark.parametrize("repeated", ["q", "k", "v", "dO"])
+@pytest.mark.parametrize("keys", ["all", "lengths", "mask", "both"])
+@pytest.mark.parametrize("nk", [90, 200])
+def test_cuda_core_kernels_in_bf16(d, h, hk, repeated, keys, nk):
+    """One token repeated in an input: forward and backward on the CUDA cores, with what the other kernels take too."""
+    gen = torch.Generator().manual_seed(d + nk)
+    b, nq = 2, 90
+    t = {}
+    for name, heads, n in (("q", h, nq), ("k", hk, nk), ("v", hk, nk), ("dO", h, nq)):
+        one = util.tokens(gen, b, heads, 1 if name == repeated else n, d, BF16, "bnhd")
+        t[name] = one.expand(b, heads, n, d)
+    p = llsa.CrossProblem(b, h, nq, nk, d, kv_heads=hk)
+    assert llsa.cross_attn_paths(p, **t) == {"fwd": "tensor" if repeated == "dO" else "cuda-core", "bwd": "cuda-core"}
+    kv_len = torch.tensor([nk, nk // 2], dtype=torch.int32, device="cuda") if keys in ("lengths", "both") else None
+    key_mask = (torch.rand(b, nk, generator=gen) < 0.7).cuda() if keys in ("mask", "both") else None
+    op = llsa.CrossAttention(p, token_major=True)
+    for x in (op.o, op.lse, op.dq, op.dk, op.dv):
+        x.fill_(math.nan)
+    op.work.fill_(255)
+    op.forward(t["q"], t["k"], t["v"], kv_len=kv_len, key_mask=key_mask)
+    op.backward_pass(t["q"], t["k"], t["v"], t["dO"], kv_len=kv_len, key_mask=key_mask)
+    torch.cuda.synchronize()
+    assert llsa.device_error() == 0
+    ok = util.valid_keys(b, nk, kv_len, key_mask)
+    for name, (want, bound) in util.cross_reference(t["q"], t["k"], t["v"], ok, p.scale, t["dO"]).items():
+        util.check(name, getattr(op, name), want, bound)
