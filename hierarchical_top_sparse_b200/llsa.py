@@ -328,7 +328,8 @@ class Pipeline:
     With qk_norm, q and k go through a layer norm over each head's channels first (``norm_q`` and ``norm_k``, eps
     `norm_eps`), with the fp32 weights and biases [d] in ``q_weight``, ``q_bias``, ``k_weight``, ``k_bias`` (ones and
     zeros at first).  Then q and k may have any batch, head and token strides; dq and dk are gradients of what was
-    passed in, and norm_q.dweight, norm_q.dbias, norm_k.dweight and norm_k.dbias those of the weights."""
+    passed in, and norm_q.dweight, norm_q.dbias, norm_k.dweight and norm_k.dbias those of the weights.  v and dO are
+    contiguous in either case; next to q and k as a projection leaves them that is checked."""
 
     def __init__(self, p: Problem, device="cuda", backward: bool = True, qk_norm: bool = False,
                  norm_eps: float = 1e-6):
@@ -363,9 +364,17 @@ class Pipeline:
             self.q_weight, self.k_weight = (torch.ones(p.d, dtype=f32, device=device) for _ in range(2))
             self.q_bias, self.k_bias = (torch.zeros(p.d, dtype=f32, device=device) for _ in range(2))
 
+    def _contiguous(self, name: str, x):
+        """Raises where x is not a tensor as the self-attention reads it, from its address alone."""
+        if not isinstance(x, int) and (x.numel() != self.o.numel() or x.dtype != self.o.dtype or
+                                       x.device != self.o.device or not x.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous {self.o.dtype} tensor of shape {tuple(self.o.shape)} on "
+                             f"{self.o.device}, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+
     def forward(self, q, k, v, stream=None):
         p = self.p
         if self.qk_norm:
+            self._contiguous("v", v)
             stream = _stream(stream)
             q = self.norm_q.forward(q, self.q_weight, self.q_bias, stream)
             k = self.norm_k.forward(k, self.k_weight, self.k_bias, stream)
@@ -380,6 +389,8 @@ class Pipeline:
         p = self.p
         x, y = q, k
         if self.qk_norm:                                    # the attention saw the normed q and k of the forward call
+            self._contiguous("v", v)
+            self._contiguous("dO", dO)
             stream = _stream(stream)
             q, k = self.norm_q.y, self.norm_k.y
         index_transpose(p, self.idx, self.offs, self.qlist, self.tscratch, stream)
