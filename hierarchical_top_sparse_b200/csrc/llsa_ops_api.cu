@@ -75,8 +75,10 @@ static llsa_status make_cross(const llsa_cross_problem* p, cross::Geo* g) {
   if (p->d % 8 != 0 || p->d > 128) return LLSA_ERR_UNSUPPORTED;
   const int64_t b = p->batch, h = p->heads, hk = p->kv_heads, nq = p->nq, nk = p->nk, d = p->d;
   if (b * h > (1 << 24) || nq > LLSA_CROSS_MAX_TOKENS || nk > LLSA_CROSS_MAX_TOKENS) return LLSA_ERR_SHAPE;
-  // a block's work between two hand-offs ends well before their waits give up
-  if (h / hk * nq > 4ll * LLSA_CROSS_MAX_TOKENS) return LLSA_ERR_SHAPE;
+  // a block's work between two hand-offs ends well before their waits give up: at most 2^19 tiles of 128 queries, each of
+  // one head where a head fills a tile (3.2 us a tile in the longest chain: 1.7 s of 4)
+  const int64_t padded = nq < 128 ? nq : (nq + 127) / 128 * 128;
+  if (h / hk * padded > 4ll * LLSA_CROSS_MAX_TOKENS) return LLSA_ERR_SHAPE;
   if (b * h * nq >= (1ll << 34) || b * hk * nk >= (1ll << 34)) return LLSA_ERR_SHAPE;
   // one block per 32 queries or keys and head at most: a grid of fewer than 2^31 blocks
   if (b * h * ((nq + 31) / 32) >= (1ll << 31) || b * hk * ((nk + 31) / 32) >= (1ll << 31)) return LLSA_ERR_SHAPE;

@@ -251,7 +251,8 @@ typedef struct {
 
 /* Cross attention: `nq` queries per head and batch row attend to the `nk`
  * states of an encoder; at most LLSA_CROSS_MAX_TOKENS of each, and four times as
- * many queries in the heads that share a key head. */
+ * many queries in the heads that share a key head (a head's 128 or more counted
+ * in whole tiles of 128). */
 #define LLSA_CROSS_MAX_TOKENS (1 << 24)
 
 typedef struct {

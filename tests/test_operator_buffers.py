@@ -1,4 +1,4 @@
-"""Buffers that the calls of cross attention and layer norm refuse before any launch (no GPU)."""
+"""Buffers and sizes that the calls of cross attention and layer norm refuse before any launch (no GPU)."""
 import ctypes
 
 import pytest
@@ -43,3 +43,14 @@ def test_norm_backward_refuses_a_misaligned_workspace():
     for dw in (GOOD, None):
         assert L.llsa_layer_norm_bwd(r, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, dw, None, GOOD + 8, None) == 3
     assert llsa.kernel_launches() == before
+
+
+@pytest.mark.parametrize("heads,nq,status", [
+    (4, 1 << 24, 0), (5, 1 << 24, 2),
+    (1 << 19, 128, 0), ((1 << 19) + 1, 128, 2),
+    (1 << 18, 129, 0), ((1 << 18) + 1, 129, 2),       # two tiles a head, one of them nearly empty
+    (1 << 19, 127, 0), (1 << 23, 8, 0),               # heads packed into tiles
+])
+def test_tiles_of_the_queries_that_share_a_key_head(heads, nq, status):
+    """A block takes a key head's query tiles one after the other, and no wait of a good run may give up."""
+    assert llsa.cross_validate(llsa.CrossProblem(batch=1, heads=heads, kv_heads=1, nq=nq, nk=200)) == status
