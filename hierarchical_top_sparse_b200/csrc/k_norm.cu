@@ -333,11 +333,15 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
                                                            float* __restrict__ part) {
   constexpr int RPB = threads<G>() / G;
   // Rows of a step and thread group.  Block-wide rows: two a barrier where that paid (50 M bf16 values, 768, 1024, 4096
-  // channels: 131, 112, 129 us against 155, 124, 156; 2048 channels 116 against 103, 25 M fp32 values of 1024 124
-  // against 86).
+  // channels: 129, 111, 125 us against 151, 122, 151), not with 256 threads (1152, 2048 channels: 165, 113 against 138,
+  // 99) nor in fp32 (25 M values, 1024, 2048 channels: 103, 114 against 83, 86).
   constexpr int R = G > 32 ? ((V == 1 && G == 128) || (V == 8 && IT == 1 && G != 256) ? 2 : 1)
                            : (V <= 2 ? (IT <= 2 ? 4 : (IT <= 4 ? 2 : 1)) : (IT > 1 ? 1 : 2));
   constexpr int NV = IT * V;
+  // A block-wide row's xhat stays in registers between its two uses, up to 16 registers of it, which undoes what the
+  // subtraction costs (50 M bf16 values of 1152, 2048, 8192 channels: 138, 99, 125 us against 149, 107, 128).  Not of
+  // single values, whose pairs are half empty (25 M fp32 values of 1001: 168 against 113), nor of narrow rows (the same).
+  constexpr bool HOLD = G > 32 && V > 1 && IT * ((V + 1) / 2) <= 8;
   __shared__ float red[G > 32 ? 2 * 2 * R * 32 : 1];
   __shared__ float cols[G <= 32 ? 8 * G * NV : 1];   // a block's eight warps' sums
   int turn = 0;
@@ -413,6 +417,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
     float sum[2 * R];
     // xhat = (x - mean) rstd, as in the forward: x rstd - mean rstd would leave the rounding of mean rstd in rows far from 0
     f2 minus[R], scale[R];
+    f2 held[HOLD ? R : 1][HOLD ? IT * P : 1];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       scale[k] = twice(rs[k]);
@@ -429,6 +434,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
 #pragma unroll
           for (int e = 0; e < P; ++e) {
             const f2 xh = mul2(add2(fx[e], minus[k]), scale[k]), gw = mul2(fg[e], ww[e]);
+            if constexpr (HOLD) held[k][i * P + e] = xh;
             s0 = add2(s0, gw);
             s1 = fma2(gw, xh, s1);
             dw[i * P + e] = fma2(fg[e], xh, dw[i * P + e]);
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(threads<G>()) bwd_kernel(const __grid_constant
           weights_of(i, ww);
 #pragma unroll
           for (int e = 0; e < P; ++e) {
-            const f2 xh = mul2(add2(fx[e], minus[k]), scale[k]);
+            const f2 xh = HOLD ? held[k][i * P + e] : mul2(add2(fx[e], minus[k]), scale[k]);
             fx[e] = fma2(fma2(xh, c2, mul2(fg[e], ww[e])), scale[k], c1);   // rstd (g - xhat c2) - rstd c1
           }
           Raw<T, V> o;
