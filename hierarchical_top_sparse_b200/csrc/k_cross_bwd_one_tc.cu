@@ -9,7 +9,7 @@
 //   dQ = scale dS K                               (M = 128 queries, complete: there is no other key tile)
 // With all keys of a row at hand D needs no O (rowsum(P o dP) = dO . O), so the
 // pass reads q, d_o and lse and writes dq: 46 us of bytes for 786432 rows of 64
-// channels, where it takes 126 us (lengths of 120 and 60 states: 383 TFLOP/s of the columns computed): the
+// channels, where it takes 128 us (lengths of 120 and 60 states: 377 TFLOP/s of the columns computed): the
 // chain from scores to dS and on, about 6000 cycles a tile, is longer.  P and dS are rounded to bf16 for the products and stand in shared
 // memory, read transposed for dV and dK (rows are then the contracted index)
 // and as they are for dQ.

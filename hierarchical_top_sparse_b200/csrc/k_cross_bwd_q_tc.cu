@@ -11,8 +11,9 @@
 // heads, 589 states, 128 channels, batch 2: 560 TFLOP/s, the rest of dS apart).  D comes from the rounded O; with dS rounded
 // as well dQ was 2.6e-3 off (relative to its norm) where the result's own
 // rounding makes 1.7e-3; the second bf16 costs products that the tensor cores
-// have time for.  Bound by the tensor cores from 128 channels
-// on, by the exponentials below.
+// have time for.  Bound by one tile's chain of hand-offs (load S, exponentials, wait for
+// dP, dS, hand over): some 6400 cycles a tile in that case, where its exponentials take
+// 1024 and its four products 2850, and no second tile of queries fills the gaps.
 //
 // Warps: 0-7 softmax, 8-11 epilogue, 12 producer of K and V (TMA), 13 MMA
 // issue, 14 fetches Q and dO (where heads are packed by plain loads) and clears
@@ -441,7 +442,8 @@ bwd_q_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
 
 }  // namespace bwdq
 
-// Key splits as in the forward: when the query tiles alone do not fill the device.
+// Key splits as in the forward, into two items an SM, rounded up: when the query
+// tiles alone do not fill the device.
 DqPlan plan_bwd_q(const Geo& g, int sms) {
   DqPlan p;
   p.packed = g.group > 1 && g.nq < kTile;

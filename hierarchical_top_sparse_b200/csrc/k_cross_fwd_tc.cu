@@ -533,9 +533,9 @@ bool fwd_tc_supported(const Geo& g) {
 }
 
 // Items: two query tiles each where that still fills the device; the keys are
-// split (whole tiles, as even as they come) when there are fewer items than
-// SMs, into four times as many as SMs at most, so that rows of unlike length
-// even out.
+// split (whole tiles, as even as they come, two at least, 64 splits at most) when
+// there are fewer items than SMs, into four items an SM, rounded up to whole
+// splits (fewer than five), so that rows of unlike length even out.
 TcPlan plan_fwd_tc(const Geo& g, int sms) {
   TcPlan p;
   p.packed = g.group > 1 && g.nq < kTile;

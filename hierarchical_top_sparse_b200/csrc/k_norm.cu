@@ -6,10 +6,13 @@
 //
 // Bound by memory: every row is read once and kept in registers as it came (the
 // variance is the mean of the squared deviations from the mean, in a second
-// pass over the registers, so that large offsets cost no digits).  G threads
+// pass over the registers, and xhat is formed from the deviation in both
+// directions, so that an offset costs what rounding it costs the mean, 2^-24 of
+// itself, and no more).  G threads
 // work on a row, each on IT vectors of 16 bytes (narrower ones, down to single
-// values, where the width, a stride or an address does not allow them); rows of up to 2 KB take a
-// part of a warp or a warp, wider ones a block.  R rows are taken at a time,
+// values, where the width, a stride or an address does not allow them).  Rows of up to
+// 2 KB take a part of a warp or a warp (in the backward of bf16 up to 1 KB, and up to 1 KB
+// or less by narrower loads), wider ones a block.  R rows are taken at a time,
 // and the next R are on their way while these are worked on: an SM needs some
 // 40 KB in flight.  Rows are walked in the order of x's memory.
 //
@@ -630,7 +633,7 @@ int bwd_parts(const Geo& g) {
 #define NORM_BOTH_SHAPES(F, T, V) \
   F(T, V, 8, 1) F(T, V, 16, 1) F(T, V, 32, 1) F(T, V, 32, 2) F(T, V, 512, 2) F(T, V, 512, 4)
 #define NORM_FWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 32, 3) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 256, 2)
-#define NORM_BWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 128, 1) F(T, V, 256, 1) F(T, V, 512, 1)
+#define NORM_BWD_SHAPES(F, T, V) NORM_BOTH_SHAPES(F, T, V) F(T, V, 256, 1) F(T, V, 512, 1)
 #define NORM_FEW_SHAPES(F, T, V) \
   F(T, V, 8, 1) F(T, V, 8, 2) F(T, V, 8, 4) F(T, V, 16, 4) F(T, V, 32, 4) F(T, V, 128, 2) F(T, V, 128, 4) \
   F(T, V, 256, 4) F(T, V, 512, 4) F(T, V, 512, 8)
@@ -680,7 +683,7 @@ cudaError_t launch_bwd(const Geo& g, const void* x, const void* dy, const void* 
     e = cudaGetLastError();                                                                                         \
   }
   if (g.bf16) {
-    NORM_BWD_SHAPES(NORM_BWD, __nv_bfloat16, 8) NORM_BWD(__nv_bfloat16, 4, 32, 3)
+    NORM_BWD_SHAPES(NORM_BWD, __nv_bfloat16, 8) NORM_BWD(__nv_bfloat16, 8, 128, 1) NORM_BWD(__nv_bfloat16, 4, 32, 3)
     NORM_FEW_SHAPES(NORM_BWD, __nv_bfloat16, 4) NORM_FEW_SHAPES(NORM_BWD, __nv_bfloat16, 2)
     NORM_BWD(__nv_bfloat16, 2, 1024, 8)
     NORM_ONE_SHAPES(NORM_BWD, __nv_bfloat16) NORM_BWD(__nv_bfloat16, 1, 256, 4) NORM_BWD(__nv_bfloat16, 1, 512, 16)
